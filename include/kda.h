@@ -380,6 +380,70 @@ KDA_API kda_status kda_chunk_prefill_host(const void *q, const void *k, const vo
                                           float *state_out, int64_t segment, void *workspace,
                                           size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Gated delta rule: the delta rule with ONE retention factor per value head
+ * and token, where KDA has one per key channel,
+ *
+ *     S_t = exp(g_t) (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T
+ *     o_t = S_t^T q_t
+ *
+ * and with key heads that groups of value heads share: value head h uses key
+ * head h / (H / Hk).  The conventions at the top of this file hold, with these
+ * differences:
+ *  - q, k are [rows, Hk, dk], v is [rows, H, dv], g and beta are [rows, H];
+ *    H is a multiple of Hk.  dk and dv are 64 or 128 each, independently.
+ *  - o has the element type `dtype` (in bf16 half the bytes of an fp32 o; the
+ *    layer's norm and projection read it in bf16).  The state is fp32 and keeps
+ *    fp32 accuracy in either type: |error| of the final state is below 1e-6 of
+ *    its norm against 64-bit arithmetic on the test inputs.
+ *  - g has no lower bound: one decay per token multiplies whole rows, so no
+ *    reciprocal is formed.  Values below -100 act as -100 (exp gives 0 beside
+ *    any representable state), -infinity among them: such a token forgets all
+ *    before it.  Values above 0 are used as given.  KDA_DEBUG_CHECKS scans
+ *    nothing here.
+ *  - q, k, v, o and the states must be 16-byte aligned (KDA_ERR_INVALID_ARG).
+ *  - rows < 2^31 - 64 and N H < 2^28, else KDA_ERR_UNSUPPORTED.
+ *  - A non-finite input makes the results of its own (sequence, head) unspecified,
+ *    tokens before it in the same 32-token chunk among them; no other unit's.
+ */
+
+/*
+ * Chunked prefill over whole sequences; arguments and cu_seqlens rules as for
+ * kda_chunk_prefill, without a workspace.  bf16 runs on the tensor cores as one
+ * launch, fp32 token by token in fp32.
+ *  q, k [B, T, Hk, dk];  v, o [B, T, H, dv];  g, beta [B, T, H]
+ *  state_in [N, H, dk, dv] or NULL (zeros); state_out or NULL (not written).
+ *  state_out may alias state_in exactly.  Rows of o that belong to no sequence
+ *  are not written.
+ */
+KDA_API kda_status kda_gdr_chunk_prefill(const void *q, const void *k, const void *v,
+                                         const void *g, const void *beta,
+                                         const float *state_in, const int32_t *cu_seqlens,
+                                         int B, int64_t T, int N, int Hk, int H, int dk, int dv,
+                                         kda_dtype dtype, void *o, float *state_out,
+                                         void *stream);
+
+/*
+ * Decode: L tokens (one, or a few drafted ones) for each of N requests, in order,
+ * on states that stay where they are.
+ *  q, k [N, L, Hk, dk];  v, o [N, L, H, dv];  g, beta [N, L, H]
+ *  state   [P, H, dk, dv] fp32.  Request n's state is entry slots[n], or entry n when
+ *          slots is NULL (then P >= N).
+ *  slots   device int32 [N], or NULL.  Must be distinct (two requests on one entry
+ *          race).  An entry outside [0, P) is skipped (its o is not written) and the
+ *          next kda_check_device_error() returns KDA_ERR_INVALID_ARG.
+ *  lens    device int32 [N], or NULL: request n takes only its first lens[n] tokens
+ *          (clamped to [0, L]); o of the others is not written.  With 0 the state
+ *          is left as it is.
+ *  update_state  0 leaves every state as it was and writes o alone: drafted tokens
+ *          are scored so, then a second call with lens = the accepted counts commits them.
+ */
+KDA_API kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const void *g,
+                                  const void *beta, float *state, const int32_t *slots,
+                                  const int32_t *lens, int N, int P, int L, int Hk, int H,
+                                  int dk, int dv, kda_dtype dtype, int update_state, void *o,
+                                  void *stream);
+
 /* Static, human-readable name of a status code. */
 KDA_API const char *kda_status_string(kda_status s);
 

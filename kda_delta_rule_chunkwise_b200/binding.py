@@ -40,6 +40,8 @@ EXPORTED = (
     "kda_chunk_prefill_static_scratch",
     "kda_prefill_host_workspace_bytes",
     "kda_chunk_prefill_host",
+    "kda_gdr_chunk_prefill",
+    "kda_gdr_decode",
     "kda_status_string",
 )
 
@@ -104,6 +106,12 @@ def load(path: str = LIB_PATH):
     lib.kda_chunk_prefill_host.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32,
                                            vp, vp, i64, vp, sz, vp]
     lib.kda_chunk_prefill_host.restype = i32
+    lib.kda_gdr_chunk_prefill.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32,
+                                          i32, i32, i32, vp, vp, vp]
+    lib.kda_gdr_chunk_prefill.restype = i32
+    lib.kda_gdr_decode.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                                   i32, i32, i32, vp, vp]
+    lib.kda_gdr_decode.restype = i32
     lib.kda_status_string.argtypes = [i32]
     lib.kda_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -377,6 +385,99 @@ def kda_decode_step_indexed(q, k, v, g, beta, state_pool, slots, *, o=None, stre
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state_pool), _ptr(slots), N,
         state_pool.shape[0], H, dk, dv, _DTYPE[q.dtype], _ptr(o), _stream(stream))
     _check(code, "kda_decode_step_indexed")
+    return o
+
+
+# ---------------------------------------------------------------- gated delta rule
+
+def _want(name, t, shape, dtype, device):
+    """Refuse a tensor of another shape, type or device than the call's."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    _contig(name, t)
+
+
+def _gdr_shapes(q, k, v, g, beta):
+    """Sizes of a gated-delta-rule call, its five inputs checked against one another."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must have four dimensions")
+    if q.dtype not in _DTYPE:
+        raise ValueError(f"q must be bf16 or fp32, got {q.dtype}")
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    B, T, Hk, dk = q.shape
+    H, dv = v.shape[2], v.shape[3]
+    for name, t, shape in (("q", q, (B, T, Hk, dk)), ("k", k, (B, T, Hk, dk)),
+                           ("v", v, (B, T, H, dv)), ("g", g, (B, T, H)),
+                           ("beta", beta, (B, T, H))):
+        _want(name, t, shape, q.dtype, q.device)
+    return B, T, Hk, H, dk, dv
+
+
+def _on(device, stream):
+    """The stream of a call on `device`: the given one, or the device's current one."""
+    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def kda_gdr_chunk_prefill(q, k, v, g, beta, state_in=None, cu_seqlens=None, *, o=None,
+                          state_out=None, want_state=True, stream=None):
+    """Chunked prefill of the gated delta rule (one decay per value head and token).
+
+    q, k: [B, T, Hk, dk]; v: [B, T, H, dv]; g, beta: [B, T, H], all bf16 or all fp32;
+    H is a multiple of Hk.  state_in: [N, H, dk, dv] fp32 or None; cu_seqlens: int32 [N+1]
+    on the device or None.  Returns (o, state_out): o like v, the state fp32.  Rows of a
+    given `o` that belong to no sequence are left as they are (zeros when allocated here).
+    """
+    B, T, Hk, H, dk, dv = _gdr_shapes(q, k, v, g, beta)
+    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    if cu_seqlens is not None:
+        _want("cu_seqlens", cu_seqlens, (max(N, 0) + 1,), torch.int32, q.device)
+    _want("state_in", state_in, (N, H, dk, dv), torch.float32, q.device)
+    _want("o", o, v.shape, q.dtype, q.device)
+    _want("state_out", state_out, (N, H, dk, dv), torch.float32, q.device)
+    if o is None:
+        new = torch.empty if cu_seqlens is None else torch.zeros
+        o = new(v.shape, dtype=q.dtype, device=q.device)
+    if state_out is None and want_state:
+        state_out = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+    with torch.cuda.device(q.device):
+        code = load().kda_gdr_chunk_prefill(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state_in), _ptr(cu_seqlens), B, T,
+            N, Hk, H, dk, dv, _DTYPE[q.dtype], _ptr(o), _ptr(state_out), _on(q.device, stream))
+    _check(code, "kda_gdr_chunk_prefill")
+    return o, state_out
+
+
+def kda_gdr_decode(q, k, v, g, beta, state, *, slots=None, lens=None, update_state=True, o=None,
+                   stream=None):
+    """L tokens for each of N requests, `state` [P, H, dk, dv] fp32 updated in place.
+
+    q, k: [N, L, Hk, dk]; v: [N, L, H, dv]; g, beta: [N, L, H].  slots: int32 [N], the pool
+    entry of each request (distinct), or None for entry n.  lens: int32 [N], tokens that each
+    request takes, or None for all L; o of the others is left as it is (zeros when allocated
+    here).  update_state=False writes o alone.  Returns o, like v.
+    """
+    N, L, Hk, H, dk, dv = _gdr_shapes(q, k, v, g, beta)
+    P = state.shape[0]
+    _want("state", state, (P, H, dk, dv), torch.float32, q.device)
+    _want("slots", slots, (N,), torch.int32, q.device)
+    _want("lens", lens, (N,), torch.int32, q.device)
+    _want("o", o, v.shape, q.dtype, q.device)
+    if o is None:
+        new = torch.empty if lens is None and slots is None else torch.zeros
+        o = new(v.shape, dtype=q.dtype, device=q.device)
+    with torch.cuda.device(q.device):
+        code = load().kda_gdr_decode(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(slots), _ptr(lens), N,
+            P, L, Hk, H, dk, dv, _DTYPE[q.dtype], 1 if update_state else 0, _ptr(o),
+            _on(q.device, stream))
+    _check(code, "kda_gdr_decode")
     return o
 
 

@@ -1,0 +1,79 @@
+// C ABI of the gated delta rule (declared in include/kda.h): argument checks, then dispatch.
+#include "gdr_launch.h"
+
+#include "kda.h"
+
+#include <climits>
+
+namespace {
+
+bool head_dim(int d) { return d == 64 || d == 128; }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+kda_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+
+// Checks shared by the calls over sequences; KDA_OK if they hold.
+kda_status check_sequences(bool packed, int B, int64_t T, int N, int Hk, int H, int dk, int dv,
+                           kda_dtype dtype) {
+    if (B < 0 || T < 0 || N < 0 || Hk <= 0 || H <= 0 || dk <= 0 || dv <= 0)
+        return KDA_ERR_INVALID_ARG;
+    if (H % Hk != 0) return KDA_ERR_INVALID_ARG;
+    if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
+    if (packed ? B != 1 : N != B) return KDA_ERR_INVALID_ARG;
+    if (!head_dim(dk) || !head_dim(dv)) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)N * H > INT32_MAX / 8) return KDA_ERR_UNSUPPORTED;
+    if (T > INT32_MAX - 64 || (B > 0 && T > (INT32_MAX - 64) / B)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_gdr_chunk_prefill(const void *q, const void *k, const void *v, const void *g,
+                                 const void *beta, const float *state_in,
+                                 const int32_t *cu_seqlens, int B, int64_t T, int N, int Hk,
+                                 int H, int dk, int dv, kda_dtype dtype, void *o,
+                                 float *state_out, void *stream) {
+    const kda_status s = check_sequences(cu_seqlens != nullptr, B, T, N, Hk, H, dk, dv, dtype);
+    if (s != KDA_OK) return s;
+    if (B * T > 0 && (!q || !k || !v || !g || !beta || !o)) return KDA_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v, (const void *)o, (const void *)state_in,
+                          (const void *)state_out})
+        if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
+    if (N == 0) return KDA_OK;
+    uint32_t *err = kda::device_error_word();
+    if (!err) return KDA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    kda::Profiler::begin(st);
+    if (dtype == KDA_BF16) {
+        const kda::GdrArgs a{q, k, v, g, beta, state_in, cu_seqlens, T, N, Hk, H, dk, dv,
+                             o, state_out, err, kda::next_launch_epoch()};
+        return from_cuda(kda::launch_gdr_prefill(a, st));
+    }
+    const kda::GdrTokenArgs a{q, k, v, g, beta, state_in, state_out, cu_seqlens, nullptr,
+                              nullptr, T, N, N, Hk, H, dk, dv, o, err};
+    return from_cuda(kda::launch_gdr_token(a, false, st));
+}
+
+kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const void *g,
+                          const void *beta, float *state, const int32_t *slots,
+                          const int32_t *lens, int N, int P, int L, int Hk, int H, int dk,
+                          int dv, kda_dtype dtype, int update_state, void *o, void *stream) {
+    if (P < 0 || L < 0) return KDA_ERR_INVALID_ARG;
+    const kda_status s = check_sequences(false, N, L, N, Hk, H, dk, dv, dtype);
+    if (s != KDA_OK) return s;
+    if (!slots && P < N) return KDA_ERR_INVALID_ARG;
+    if (N > 0 && L > 0 && (!q || !k || !v || !g || !beta || !state || !o))
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned16(state)) return KDA_ERR_INVALID_ARG;
+    if (N == 0 || L == 0) return KDA_OK;
+    uint32_t *err = kda::device_error_word();
+    if (!err) return KDA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    kda::Profiler::begin(st);
+    const kda::GdrTokenArgs a{q, k, v, g, beta, state, update_state ? state : nullptr, nullptr,
+                              slots, lens, L, N, P, Hk, H, dk, dv, o, err};
+    return from_cuda(kda::launch_gdr_token(a, dtype == KDA_BF16, st));
+}
+
+}  // extern "C"

@@ -1,0 +1,173 @@
+// Gated delta rule, token by token in fp32: the decode step (one or a few tokens per
+// request, either input type) and the prefill of fp32 inputs.
+//
+// Per (request n, value head h) and token, with a = exp(g):
+//     p = S^T k;  y = S^T q;  delta = beta (v - a p);  o = a y + (k.q) delta
+//     S <- a S + k delta^T
+// so one pass over the state gives both sums, and a second one updates it.
+//
+// One decode token is bound by HBM: each state (dk x dv fp32, 64 KiB at d = 128) is read
+// and written once, everything else is about 1 KiB.  With L tokens the state stays in
+// registers between them, so they cost one pass over it as well.
+//
+// One CTA of 256 threads per (n, h, slice of DVS columns).  A thread keeps a
+// (DK / RG) x 4 block of S in registers, loaded as coalesced 16-byte vectors.  The sums
+// over channels are taken over a thread's rows, over the lanes of a warp that hold the
+// same columns, and over the eight warps through shared memory, always in the same order.
+// Inputs of the next token are loaded while this one is computed; buffers alternate, so a
+// token costs two barriers.
+#include "gdr_common.cuh"
+#include "gdr_launch.h"
+
+namespace kda {
+namespace gdr {
+
+template <int DK, int DVS, typename Tin>
+__global__ void __launch_bounds__(256) gdr_token_kernel(GdrTokenArgs a) {
+    constexpr int NT = 256, CG = DVS / 4, RG = NT / CG, RPT = DK / RG, NW = NT / 32;
+    static_assert(CG <= 32 && DK % RG == 0, "a warp covers whole rows");
+    const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG, warp = tid >> 5, lane = tid & 31;
+    const int slices = a.dv / DVS;
+    const int slice = blockIdx.x % slices, unit = blockIdx.x / slices;
+    const int h = unit % a.H, n = unit / a.H, hk = h / (a.H / a.Hk);
+
+    const Span span = sequence_span(a.cu_seqlens, n, a.T);
+    int len = span.len;
+    if (a.lens) len = min(max(a.lens[n], 0), len);
+    int64_t entry = n;
+    if (a.slots) {
+        const int slot = a.slots[n];
+        if (slot < 0 || slot >= a.P) {
+            if (tid == 0 && h == 0 && slice == 0 && a.err) atomicOr(a.err, ERR_BAD_INDEX);
+            return;
+        }
+        entry = slot;
+    }
+    if (len == 0 && (a.state_out == nullptr || a.state_out == a.state_in)) return;
+    const int64_t soff = (entry * a.H + h) * DK * a.dv + slice * DVS;
+
+    __shared__ float ks[2][DK], qs[2][DK], vs[2][DVS], gb[2][2];
+    __shared__ float4 red_p[2][NW][CG], red_y[2][NW][CG];
+    __shared__ float dl[2][DVS], kq[2];
+
+    float4 s[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+        s[i] = a.state_in ? __ldcs(reinterpret_cast<const float4 *>(
+                                a.state_in + soff + (int64_t)(rg + i * RG) * a.dv) + cg)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+
+    // one element of k, q or v per thread: DK + DK + DVS of them, DK of q by the upper half
+    const Tin *q = (const Tin *)a.q, *k = (const Tin *)a.k, *v = (const Tin *)a.v;
+    float in_k = 0.f, in_v = 0.f, in_g = 0.f;
+    auto fetch = [&](int t) {
+        const int64_t row = span.row + t;
+        if (tid < DK) in_k = to_f32(k[(row * a.Hk + hk) * DK + tid]);
+        else if (tid >= 128 && tid < 128 + DK) in_k = to_f32(q[(row * a.Hk + hk) * DK + tid - 128]);
+        if (tid < DVS) in_v = to_f32(v[(row * a.H + h) * a.dv + slice * DVS + tid]);
+        if (tid == 0) in_g = to_f32(((const Tin *)a.g)[row * a.H + h]);
+        if (tid == 32) in_g = to_f32(((const Tin *)a.beta)[row * a.H + h]);
+    };
+    auto publish = [&](int b) {
+        if (tid < DK) ks[b][tid] = in_k;
+        else if (tid >= 128 && tid < 128 + DK) qs[b][tid - 128] = in_k;
+        if (tid < DVS) vs[b][tid] = in_v;
+        if (tid == 0) gb[b][0] = expf(fmaxf(in_g, kMinLogDecay));
+        if (tid == 32) gb[b][1] = in_g;
+    };
+    if (len > 0) {
+        fetch(0);
+        publish(0);
+    }
+    __syncthreads();
+    for (int t = 0; t < len; ++t) {
+        const int b = t & 1;
+        if (t + 1 < len) fetch(t + 1);
+        float4 p = make_float4(0.f, 0.f, 0.f, 0.f), y = p;
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            const float kr = ks[b][rg + i * RG], qr = qs[b][rg + i * RG];
+            p.x = fmaf(s[i].x, kr, p.x); p.y = fmaf(s[i].y, kr, p.y);
+            p.z = fmaf(s[i].z, kr, p.z); p.w = fmaf(s[i].w, kr, p.w);
+            y.x = fmaf(s[i].x, qr, y.x); y.y = fmaf(s[i].y, qr, y.y);
+            y.z = fmaf(s[i].z, qr, y.z); y.w = fmaf(s[i].w, qr, y.w);
+        }
+#pragma unroll
+        for (int m = CG; m < 32; m <<= 1) {
+            p.x += __shfl_xor_sync(0xffffffffu, p.x, m); p.y += __shfl_xor_sync(0xffffffffu, p.y, m);
+            p.z += __shfl_xor_sync(0xffffffffu, p.z, m); p.w += __shfl_xor_sync(0xffffffffu, p.w, m);
+            y.x += __shfl_xor_sync(0xffffffffu, y.x, m); y.y += __shfl_xor_sync(0xffffffffu, y.y, m);
+            y.z += __shfl_xor_sync(0xffffffffu, y.z, m); y.w += __shfl_xor_sync(0xffffffffu, y.w, m);
+        }
+        if (lane < CG) {
+            red_p[b][warp][lane] = p;
+            red_y[b][warp][lane] = y;
+        }
+        if (warp == NW - 1) {
+            float d = 0.f;
+#pragma unroll
+            for (int c = 0; c < DK; c += 32) d = fmaf(ks[b][c + lane], qs[b][c + lane], d);
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+            if (lane == 0) kq[b] = d;
+        }
+        if (t + 1 < len) publish(b ^ 1);
+        __syncthreads();
+        const float dec = gb[b][0];
+        if (tid < DVS) {
+            float pj = 0.f, yj = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                pj += reinterpret_cast<const float *>(&red_p[b][w][0])[tid];
+                yj += reinterpret_cast<const float *>(&red_y[b][w][0])[tid];
+            }
+            const float d = gb[b][1] * (vs[b][tid] - dec * pj);
+            dl[b][tid] = d;
+            ((Tin *)a.o)[((span.row + t) * a.H + h) * a.dv + slice * DVS + tid] =
+                from_f32<Tin>(fmaf(kq[b], d, dec * yj));
+        }
+        __syncthreads();
+        const float4 d4 = reinterpret_cast<const float4 *>(dl[b])[cg];
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            const float kr = ks[b][rg + i * RG];
+            s[i].x = fmaf(kr, d4.x, dec * s[i].x); s[i].y = fmaf(kr, d4.y, dec * s[i].y);
+            s[i].z = fmaf(kr, d4.z, dec * s[i].z); s[i].w = fmaf(kr, d4.w, dec * s[i].w);
+        }
+    }
+    if (a.state_out) {
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+            __stcs(reinterpret_cast<float4 *>(a.state_out + soff + (int64_t)(rg + i * RG) * a.dv) + cg,
+                   s[i]);
+    }
+}
+
+template <int DK, int DVS, typename Tin>
+static cudaError_t launch_token_t(const GdrTokenArgs &a, cudaStream_t st) {
+    const int64_t grid = (int64_t)a.N * a.H * (a.dv / DVS);
+    gdr_token_kernel<DK, DVS, Tin><<<(unsigned)grid, 256, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    Profiler::mark(st);
+    return e;
+}
+
+template <int DK, typename Tin>
+static cudaError_t launch_token_d(const GdrTokenArgs &a, cudaStream_t st) {
+    // few (request, head) units: narrow slices, so that more SMs read the states
+    const int64_t units = (int64_t)a.N * a.H;
+    if (units * (a.dv / 32) <= 2 * 148) return launch_token_t<DK, 32, Tin>(a, st);
+    return a.dv == 64 ? launch_token_t<DK, 64, Tin>(a, st) : launch_token_t<DK, 128, Tin>(a, st);
+}
+
+}  // namespace gdr
+
+cudaError_t launch_gdr_token(const GdrTokenArgs &a, bool bf16, cudaStream_t st) {
+    if (a.dk == 64)
+        return bf16 ? gdr::launch_token_d<64, __nv_bfloat16>(a, st)
+                    : gdr::launch_token_d<64, float>(a, st);
+    return bf16 ? gdr::launch_token_d<128, __nv_bfloat16>(a, st)
+                : gdr::launch_token_d<128, float>(a, st);
+}
+
+}  // namespace kda

@@ -52,6 +52,8 @@ std::mutex g_prof_mu;
 
 namespace kda {
 
+uint32_t *device_error_word() { return error_word_ptr(); }
+
 uint32_t next_launch_epoch() {
     uint32_t e;
     do {

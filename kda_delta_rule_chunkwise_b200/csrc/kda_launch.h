@@ -34,6 +34,9 @@ struct PrefillArgs {
 // A fresh nonzero epoch for one launch of kernels that use bounded waits.
 uint32_t next_launch_epoch();
 
+// The current device's error area (kda_common.cuh), or nullptr if it cannot be had.
+uint32_t *device_error_word();
+
 // Optional per-kernel event recording (see kda_profile_enable).  Launchers
 // call mark() before their first kernel and after each kernel.
 struct Profiler {

@@ -1,0 +1,73 @@
+"""What the gated-delta-rule calls refuse, before anything is launched (no device needed)."""
+import pytest
+import torch
+
+from kda_delta_rule_chunkwise_b200 import binding
+from kda_delta_rule_chunkwise_b200 import build as kbuild
+
+BAD, NOT = binding.KDA_ERR_INVALID_ARG, binding.KDA_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def lib():
+    kbuild.build()
+    return binding.load()
+
+
+def prefill(lib, **kw):
+    a = dict(q=16, k=32, v=48, g=64, beta=80, state_in=None, cu=None, B=1, T=16, N=1, Hk=2, H=4, dk=128, dv=128,
+             dtype=binding.KDA_BF16, o=96, state_out=None, stream=None)
+    a.update(kw)
+    return lib.kda_gdr_chunk_prefill(*a.values())
+
+
+@pytest.mark.parametrize("bad", [
+    dict(B=-1), dict(T=-1), dict(N=-1), dict(N=2), dict(Hk=0), dict(H=0), dict(Hk=3), dict(dk=0), dict(dv=-64),
+    dict(dtype=2), dict(cu=4, B=2, N=2), dict(q=None), dict(k=None), dict(v=None), dict(g=None), dict(beta=None),
+    dict(o=None), dict(q=17), dict(k=40), dict(v=8), dict(o=100), dict(state_in=4), dict(state_out=8)])
+def test_prefill_refuses(lib, bad):
+    assert prefill(lib, **bad) == BAD
+
+
+@pytest.mark.parametrize("bad", [dict(dk=96), dict(dv=32), dict(dk=256), dict(T=2 ** 31), dict(B=2 ** 16, N=2 ** 16, T=2 ** 16),
+                                 dict(cu=4, N=2 ** 28)])
+def test_prefill_does_not_support(lib, bad):
+    assert prefill(lib, **bad) == NOT
+
+
+def test_prefill_of_nothing(lib):
+    assert prefill(lib, B=0, N=0, q=None, k=None, v=None, g=None, beta=None, o=None) == binding.KDA_OK
+
+
+def decode(lib, **kw):
+    a = dict(q=16, k=32, v=48, g=64, beta=80, state=96, slots=None, lens=None, N=4, P=4, L=1, Hk=2, H=4, dk=128, dv=64,
+             dtype=binding.KDA_BF16, update=1, o=112, stream=None)
+    a.update(kw)
+    return lib.kda_gdr_decode(*a.values())
+
+
+@pytest.mark.parametrize("bad", [dict(N=-1), dict(P=-1), dict(P=3), dict(L=-1), dict(H=5), dict(dtype=9), dict(q=None),
+                                 dict(state=None), dict(o=None), dict(state=100), dict(Hk=0)])
+def test_decode_refuses(lib, bad):
+    assert decode(lib, **bad) == BAD
+
+
+def test_decode_sizes(lib):
+    assert decode(lib, dk=32) == NOT and decode(lib, N=2 ** 27, P=2 ** 27) == NOT
+    assert decode(lib, N=0, P=0) == binding.KDA_OK and decode(lib, L=0) == binding.KDA_OK
+
+
+def test_binding_refuses_other_shapes_types_and_devices():
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    v, g = torch.zeros(1, 4, 4, 64, dtype=torch.bfloat16), torch.zeros(1, 4, 4, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        binding.kda_gdr_chunk_prefill(q, q, v, g, g)
+    with pytest.raises(ValueError, match="bf16 or fp32"):
+        binding.kda_gdr_chunk_prefill(q.half(), q, v, g, g)
+    with pytest.raises(ValueError, match="four dimensions"):
+        binding.kda_gdr_decode(q[0], q[0], v[0], g[0], g[0], torch.zeros(1, 4, 64, 64))
+    for bad, match in ((q[:, :2], "shape"), (q.float(), "must be torch.bfloat16")):
+        with pytest.raises(ValueError, match=match):
+            binding._want("k", bad, q.shape, q.dtype, q.device)
+    with pytest.raises(ValueError, match="contiguous"):
+        binding._want("k", q.transpose(1, 2), (1, 2, 4, 64), q.dtype, q.device)
