@@ -444,6 +444,46 @@ KDA_API kda_status kda_gdr_decode(const void *q, const void *k, const void *v, c
                                   int dk, int dv, kda_dtype dtype, int update_state, void *o,
                                   void *stream);
 
+/* ------------------------------------------------------------------------
+ * Block norm: closes one block of a model (this library's attention, or any
+ * other) and opens the next, in one pass over the rows:
+ *
+ *     n  = y / rms(y) * w_post            rms(z) = sqrt(mean z^2 + eps)
+ *     x' = x + scale * sigmoid(gate) * n
+ *     h  = x' / rms(x') * w_pre
+ *
+ *  x       [rows, width] residual stream, x_dtype;  x_new = x' likewise
+ *  y, gate [rows, width] the block's output and its gate's logits, dtype; gate NULL
+ *          means no gate (a factor of 1)
+ *  w_post, w_pre [width], dtype;  h [rows, width], dtype
+ *  width 1 .. 16384; widths that are a multiple of 8 with 16-byte aligned tensors take
+ *  the vector path.  eps > 0.  x_dtype is dtype, or KDA_F32 beside KDA_BF16 (a residual
+ *  stream kept in fp32); KDA_BF16 beside KDA_F32 is KDA_ERR_UNSUPPORTED.
+ *  Arithmetic is fp32, each output is rounded once; h is the norm of the unrounded x'.
+ *  x_new may alias x exactly, and h may alias y or gate exactly.
+ */
+KDA_API kda_status kda_block_norm(const void *x, const void *y, const void *gate,
+                                  const void *w_post, const void *w_pre, int64_t rows, int width,
+                                  float scale, float eps, kda_dtype x_dtype, kda_dtype dtype,
+                                  void *x_new, void *h, void *stream);
+
+/*
+ * Its gradients, from dx_new = dL/dx' (x_dtype) and dh = dL/dh (dtype), either NULL for
+ * zeros: dx (x_dtype), dy and dgate (dtype; dgate only with a gate), and the weights'
+ * dw_post and dw_pre [width], fp32, summed over the rows in a fixed order.  x' is formed
+ * again from x, y and gate.  dx may alias x or dx_new exactly, dy may alias y or dh, dgate
+ * may alias gate (each output one input of its own).
+ *  workspace  at least kda_block_norm_backward_workspace_bytes() bytes, 4-byte aligned
+ */
+KDA_API size_t kda_block_norm_backward_workspace_bytes(int64_t rows, int width);
+KDA_API kda_status kda_block_norm_backward(const void *x, const void *y, const void *gate,
+                                           const void *w_post, const void *w_pre,
+                                           const void *dx_new, const void *dh, int64_t rows,
+                                           int width, float scale, float eps, kda_dtype x_dtype,
+                                           kda_dtype dtype, void *dx, void *dy, void *dgate,
+                                           float *dw_post, float *dw_pre, void *workspace,
+                                           size_t workspace_bytes, void *stream);
+
 /* Static, human-readable name of a status code. */
 KDA_API const char *kda_status_string(kda_status s);
 

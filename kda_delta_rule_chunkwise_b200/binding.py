@@ -42,6 +42,9 @@ EXPORTED = (
     "kda_chunk_prefill_host",
     "kda_gdr_chunk_prefill",
     "kda_gdr_decode",
+    "kda_block_norm",
+    "kda_block_norm_backward_workspace_bytes",
+    "kda_block_norm_backward",
     "kda_status_string",
 )
 
@@ -112,6 +115,14 @@ def load(path: str = LIB_PATH):
     lib.kda_gdr_decode.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
                                    i32, i32, i32, vp, vp]
     lib.kda_gdr_decode.restype = i32
+    f32 = ctypes.c_float
+    lib.kda_block_norm.argtypes = [vp, vp, vp, vp, vp, i64, i32, f32, f32, i32, i32, vp, vp, vp]
+    lib.kda_block_norm.restype = i32
+    lib.kda_block_norm_backward_workspace_bytes.argtypes = [i64, i32]
+    lib.kda_block_norm_backward_workspace_bytes.restype = sz
+    lib.kda_block_norm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, f32, f32, i32, i32,
+                                            vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_block_norm_backward.restype = i32
     lib.kda_status_string.argtypes = [i32]
     lib.kda_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -479,6 +490,98 @@ def kda_gdr_decode(q, k, v, g, beta, state, *, slots=None, lens=None, update_sta
             _on(q.device, stream))
     _check(code, "kda_gdr_decode")
     return o
+
+
+# ---------------------------------------------------------------- block norm
+
+def _norm_shapes(x, y, gate, w_post, w_pre):
+    """(rows, width) of a block-norm call, its inputs checked against one another."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have a last dimension of at least 1")
+    if x.dtype not in _DTYPE or y.dtype not in _DTYPE:
+        raise ValueError(f"x and y must be bf16 or fp32, got {x.dtype} and {y.dtype}")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    D = x.shape[-1]
+    _want("x", x, x.shape, x.dtype, x.device)
+    for name, t, shape in (("y", y, x.shape), ("gate", gate, x.shape), ("w_post", w_post, (D,)),
+                           ("w_pre", w_pre, (D,))):
+        _want(name, t, shape, y.dtype, x.device)
+    return x.numel() // D, D
+
+
+def kda_block_norm(x, y, gate, w_post, w_pre, *, scale=1.0, eps=1e-6, x_new=None, h=None,
+                   stream=None):
+    """Norm after a block, its gate, the scaled residual sum and the norm before the next block:
+
+        x' = x + scale * sigmoid(gate) * y / rms(y) * w_post,   h = x' / rms(x') * w_pre
+
+    x: [..., D], bf16 or fp32; y and gate (logits, or None for no gate) like x, w_post and
+    w_pre [D], all of y's dtype (x may be fp32 beside bf16).  Returns (x', h): x' like x, h
+    like y.  x_new may be x itself (in place).
+    """
+    rows, D = _norm_shapes(x, y, gate, w_post, w_pre)
+    _want("x_new", x_new, x.shape, x.dtype, x.device)
+    _want("h", h, y.shape, y.dtype, x.device)
+    x_new = torch.empty_like(x) if x_new is None else x_new
+    h = torch.empty_like(y) if h is None else h
+    with torch.cuda.device(x.device):
+        code = load().kda_block_norm(
+            _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(w_pre), rows, D, float(scale),
+            float(eps), _DTYPE[x.dtype], _DTYPE[y.dtype], _ptr(x_new), _ptr(h),
+            _on(x.device, stream))
+    _check(code, "kda_block_norm")
+    return x_new, h
+
+
+def kda_block_norm_backward(x, y, gate, w_post, w_pre, dx_new, dh, *, scale=1.0, eps=1e-6,
+                            workspace=None, stream=None):
+    """Gradients of kda_block_norm from those of its outputs (either may be None).
+
+    Returns (dx, dy, dgate, dw_post, dw_pre): dx like x, dy and dgate like y (dgate None without
+    a gate), the weights' gradients fp32."""
+    rows, D = _norm_shapes(x, y, gate, w_post, w_pre)
+    _want("dx_new", dx_new, x.shape, x.dtype, x.device)
+    _want("dh", dh, y.shape, y.dtype, x.device)
+    dx, dy = torch.empty_like(x), torch.empty_like(y)
+    dgate = None if gate is None else torch.empty_like(gate)
+    dw = torch.empty((2, D), dtype=torch.float32, device=x.device)
+    need = int(load().kda_block_norm_backward_workspace_bytes(rows, D))
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with torch.cuda.device(x.device):
+        code = load().kda_block_norm_backward(
+            _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(dx_new), _ptr(dh), rows,
+            D, float(scale), float(eps), _DTYPE[x.dtype], _DTYPE[y.dtype], _ptr(dx), _ptr(dy),
+            _ptr(dgate), _ptr(dw[0]), _ptr(dw[1]), _ptr(workspace), ws_bytes, _on(x.device, stream))
+    _check(code, "kda_block_norm_backward")
+    return dx, dy, dgate, dw[0], dw[1]
+
+
+class KDABlockNorm(torch.autograd.Function):
+    """The block norm as a differentiable op: kda_block_norm and kda_block_norm_backward
+    (the weights' fp32 gradients cast to their dtype).  Returns (x', h)."""
+
+    @staticmethod
+    def forward(ctx, x, y, gate, w_post, w_pre, scale=1.0, eps=1e-6):
+        ctx.save_for_backward(x, y, gate, w_post, w_pre)
+        ctx.scale, ctx.eps = scale, eps
+        ctx.set_materialize_grads(False)
+        return kda_block_norm(x, y, gate, w_post, w_pre, scale=scale, eps=eps)
+
+    @staticmethod
+    def backward(ctx, dx_new, dh):
+        x, y, gate, w_post, w_pre = ctx.saved_tensors
+        dx, dy, dgate, dwo, dwi = kda_block_norm_backward(
+            x, y, gate, w_post, w_pre, None if dx_new is None else dx_new.contiguous(),
+            None if dh is None else dh.contiguous(), scale=ctx.scale, eps=ctx.eps)
+        return dx, dy, dgate, dwo.to(w_post.dtype), dwi.to(w_pre.dtype), None, None
+
+
+def kda_block_norm_autograd(x, y, gate, w_post, w_pre, scale=1.0, eps=1e-6):
+    """Differentiable block norm (see KDABlockNorm): (x', h)."""
+    return KDABlockNorm.apply(x, y, gate, w_post, w_pre, scale, eps)
 
 
 def kda_check_device_error(stream=None) -> int:

@@ -1,9 +1,12 @@
-// C ABI of the gated delta rule (declared in include/kda.h): argument checks, then dispatch.
+// C ABI of the gated delta rule and the block norm (declared in include/kda.h): argument
+// checks, then dispatch.
+#include "block_norm.h"
 #include "gdr_launch.h"
 
 #include "kda.h"
 
 #include <climits>
+#include <cmath>
 
 namespace {
 
@@ -22,6 +25,18 @@ kda_status check_sequences(bool packed, int B, int64_t T, int N, int Hk, int H, 
     if (!head_dim(dk) || !head_dim(dv)) return KDA_ERR_UNSUPPORTED;
     if ((int64_t)N * H > INT32_MAX / 8) return KDA_ERR_UNSUPPORTED;
     if (T > INT32_MAX - 64 || (B > 0 && T > (INT32_MAX - 64) / B)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// Checks shared by the block norm's two directions.
+kda_status check_norm(int64_t rows, int width, float scale, float eps, kda_dtype x_dtype,
+                      kda_dtype dtype) {
+    if (rows < 0 || width <= 0 || !std::isfinite(scale) || !(eps > 0.f) || !std::isfinite(eps))
+        return KDA_ERR_INVALID_ARG;
+    for (kda_dtype t : {x_dtype, dtype})
+        if (t != KDA_F32 && t != KDA_BF16) return KDA_ERR_INVALID_ARG;
+    if (x_dtype == KDA_BF16 && dtype == KDA_F32) return KDA_ERR_UNSUPPORTED;
+    if (width > kda::kBlockNormMaxWidth || rows > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -74,6 +89,48 @@ kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const voi
     const kda::GdrTokenArgs a{q, k, v, g, beta, state, update_state ? state : nullptr, nullptr,
                               slots, lens, L, N, P, Hk, H, dk, dv, o, err};
     return from_cuda(kda::launch_gdr_token(a, dtype == KDA_BF16, st));
+}
+
+kda_status kda_block_norm(const void *x, const void *y, const void *gate, const void *w_post,
+                          const void *w_pre, int64_t rows, int width, float scale, float eps,
+                          kda_dtype x_dtype, kda_dtype dtype, void *x_new, void *h,
+                          void *stream) {
+    const kda_status s = check_norm(rows, width, scale, eps, x_dtype, dtype);
+    if (s != KDA_OK) return s;
+    if (rows == 0) return KDA_OK;
+    if (!x || !y || !w_post || !w_pre || !x_new || !h) return KDA_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    kda::Profiler::begin(st);
+    kda::BlockNormArgs a{x, y, gate, w_post, w_pre, rows, width, scale, eps, x_new, h};
+    return from_cuda(kda::launch_block_norm(a, x_dtype == KDA_BF16, dtype == KDA_BF16, false, st));
+}
+
+size_t kda_block_norm_backward_workspace_bytes(int64_t rows, int width) {
+    if (rows < 0 || width <= 0 || width > kda::kBlockNormMaxWidth) return 0;
+    return kda::block_norm_parts(rows, width) * 2 * (size_t)width * sizeof(float);
+}
+
+kda_status kda_block_norm_backward(const void *x, const void *y, const void *gate,
+                                   const void *w_post, const void *w_pre, const void *dx_new,
+                                   const void *dh, int64_t rows, int width, float scale,
+                                   float eps, kda_dtype x_dtype, kda_dtype dtype, void *dx,
+                                   void *dy, void *dgate, float *dw_post, float *dw_pre,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+    const kda_status s = check_norm(rows, width, scale, eps, x_dtype, dtype);
+    if (s != KDA_OK) return s;
+    if (!dw_post || !dw_pre) return KDA_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || !y || !w_post || !w_pre || !dx || !dy || (gate && !dgate)))
+        return KDA_ERR_INVALID_ARG;
+    const size_t need = kda_block_norm_backward_workspace_bytes(rows, width);
+    if (need > 0 && (!workspace || workspace_bytes < need ||
+                     (reinterpret_cast<uintptr_t>(workspace) & 3u) != 0))
+        return KDA_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    kda::Profiler::begin(st);
+    kda::BlockNormArgs a{x, y, gate, w_post, w_pre, rows, width, scale, eps, nullptr, nullptr,
+                         dx_new, dh, dx, dy, dgate, dw_post, dw_pre,
+                         static_cast<float *>(workspace)};
+    return from_cuda(kda::launch_block_norm(a, x_dtype == KDA_BF16, dtype == KDA_BF16, true, st));
 }
 
 }  // extern "C"
