@@ -444,6 +444,27 @@ KDA_API kda_status kda_gdr_decode(const void *q, const void *k, const void *v, c
                                   int dk, int dv, kda_dtype dtype, int update_state, void *o,
                                   void *stream);
 
+/*
+ * Backward of the recurrence: given dout = dL/do (like o) and dstate_out = dL/dS_final
+ * ([N, H, dk, dv] fp32, or NULL for zeros), writes dq, dk_out (like q, summed over the value
+ * heads that share a key head), dv_out (like v), dg and dbeta (like g), each in `dtype` and
+ * for every row that belongs to a sequence, and dstate_in = dL/dS_0 (fp32, or NULL: not
+ * written).  Inputs as for the forward call.  bf16 runs on the tensor cores in three launches;
+ * sums have a fixed order, so results are the same on every run.
+ *  dout and the gradients of q, k, v and the states must be 16-byte aligned.
+ *  workspace  at least kda_gdr_backward_workspace_bytes() bytes, 256-byte aligned; its
+ *             contents are read only within the call.
+ */
+KDA_API size_t kda_gdr_backward_workspace_bytes(int64_t rows, int N, int Hk, int H, int dk, int dv,
+                                                kda_dtype dtype);
+KDA_API kda_status kda_gdr_backward(const void *q, const void *k, const void *v, const void *g,
+                                    const void *beta, const float *state_in,
+                                    const int32_t *cu_seqlens, int B, int64_t T, int N, int Hk,
+                                    int H, int dk, int dv, kda_dtype dtype, const void *dout,
+                                    const float *dstate_out, void *dq, void *dk_out, void *dv_out,
+                                    void *dg, void *dbeta, float *dstate_in, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------------
  * Block norm: closes one block of a model (this library's attention, or any
  * other) and opens the next, in one pass over the rows:

@@ -42,6 +42,8 @@ EXPORTED = (
     "kda_chunk_prefill_host",
     "kda_gdr_chunk_prefill",
     "kda_gdr_decode",
+    "kda_gdr_backward_workspace_bytes",
+    "kda_gdr_backward",
     "kda_block_norm",
     "kda_block_norm_backward_workspace_bytes",
     "kda_block_norm_backward",
@@ -115,6 +117,11 @@ def load(path: str = LIB_PATH):
     lib.kda_gdr_decode.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
                                    i32, i32, i32, vp, vp]
     lib.kda_gdr_decode.restype = i32
+    lib.kda_gdr_backward_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32]
+    lib.kda_gdr_backward_workspace_bytes.restype = sz
+    lib.kda_gdr_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32, i32,
+                                     i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_gdr_backward.restype = i32
     f32 = ctypes.c_float
     lib.kda_block_norm.argtypes = [vp, vp, vp, vp, vp, i64, i32, f32, f32, i32, i32, vp, vp, vp]
     lib.kda_block_norm.restype = i32
@@ -490,6 +497,59 @@ def kda_gdr_decode(q, k, v, g, beta, state, *, slots=None, lens=None, update_sta
             _on(q.device, stream))
     _check(code, "kda_gdr_decode")
     return o
+
+
+def kda_gdr_backward(q, k, v, g, beta, state_in, cu_seqlens, dout, dstate_out=None, *,
+                     want_dstate_in=True, workspace=None, stream=None):
+    """Gradients of the gated delta rule: (dq, dk, dv, dg, dbeta, dstate_in), each of its input's
+    type (dstate_in fp32, None unless want_dstate_in).  Inputs as for kda_gdr_chunk_prefill;
+    dout like o.  Rows that belong to no sequence get zeros."""
+    B, T, Hk, H, dk, dv = _gdr_shapes(q, k, v, g, beta)
+    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    if cu_seqlens is not None:
+        _want("cu_seqlens", cu_seqlens, (max(N, 0) + 1,), torch.int32, q.device)
+    _want("state_in", state_in, (N, H, dk, dv), torch.float32, q.device)
+    _want("dout", dout, v.shape, q.dtype, q.device)
+    _want("dstate_out", dstate_out, (N, H, dk, dv), torch.float32, q.device)
+    new = torch.empty_like if cu_seqlens is None else torch.zeros_like
+    dq, dk_, dv_, dg, db = new(q), new(k), new(v), new(g), new(beta)
+    ds0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device) if want_dstate_in else None
+    need = int(load().kda_gdr_backward_workspace_bytes(B * T, N, Hk, H, dk, dv, _DTYPE[q.dtype]))
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    with torch.cuda.device(q.device):
+        code = load().kda_gdr_backward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state_in), _ptr(cu_seqlens), B, T,
+            N, Hk, H, dk, dv, _DTYPE[q.dtype], _ptr(dout), _ptr(dstate_out), _ptr(dq), _ptr(dk_),
+            _ptr(dv_), _ptr(dg), _ptr(db), _ptr(ds0), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _on(q.device, stream))
+    _check(code, "kda_gdr_backward")
+    return dq, dk_, dv_, dg, db, ds0
+
+
+class KDAGatedDeltaRule(torch.autograd.Function):
+    """The gated-delta-rule prefill as a differentiable op: forward is kda_gdr_chunk_prefill,
+    backward kda_gdr_backward.  Returns (o, state_out); cu_seqlens gets no gradient."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, state_in=None, cu_seqlens=None):
+        o, s = kda_gdr_chunk_prefill(q, k, v, g, beta, state_in, cu_seqlens)
+        ctx.save_for_backward(q, k, v, g, beta, state_in, cu_seqlens)
+        ctx.set_materialize_grads(False)
+        return o, s
+
+    @staticmethod
+    def backward(ctx, do, dstate):
+        q, k, v, g, beta, state_in, cu = ctx.saved_tensors
+        do = torch.zeros_like(v) if do is None else do.contiguous()
+        return (*kda_gdr_backward(q, k, v, g, beta, state_in, cu, do,
+                                  None if dstate is None else dstate.contiguous(),
+                                  want_dstate_in=state_in is not None), None)
+
+
+def kda_gdr_autograd(q, k, v, g, beta, state_in=None, cu_seqlens=None):
+    """Differentiable gated-delta-rule prefill (see KDAGatedDeltaRule): (o, state_out)."""
+    return KDAGatedDeltaRule.apply(q, k, v, g, beta, state_in, cu_seqlens)
 
 
 # ---------------------------------------------------------------- block norm

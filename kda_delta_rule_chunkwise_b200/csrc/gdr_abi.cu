@@ -91,6 +91,44 @@ kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const voi
     return from_cuda(kda::launch_gdr_token(a, dtype == KDA_BF16, st));
 }
 
+size_t kda_gdr_backward_workspace_bytes(int64_t rows, int N, int Hk, int H, int dk, int dv,
+                                        kda_dtype dtype) {
+    if (rows < 0 || N < 0 || Hk <= 0 || H <= 0 || H % Hk != 0 || !head_dim(dk) || !head_dim(dv))
+        return 0;
+    return kda::gdr_backward_workspace_bytes(rows, N, H, dk, dv, dtype == KDA_BF16);
+}
+
+kda_status kda_gdr_backward(const void *q, const void *k, const void *v, const void *g,
+                            const void *beta, const float *state_in, const int32_t *cu_seqlens,
+                            int B, int64_t T, int N, int Hk, int H, int dk, int dv,
+                            kda_dtype dtype, const void *dout, const float *dstate_out, void *dq,
+                            void *dk_out, void *dv_out, void *dg, void *dbeta, float *dstate_in,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    const kda_status s = check_sequences(cu_seqlens != nullptr, B, T, N, Hk, H, dk, dv, dtype);
+    if (s != KDA_OK) return s;
+    const int64_t rows = B * T;
+    if (rows > 0 && (!q || !k || !v || !g || !beta || !dout || !dq || !dk_out || !dv_out || !dg ||
+                     !dbeta))
+        return KDA_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v, dout, (const void *)state_in, (const void *)dstate_out,
+                          (const void *)dq, (const void *)dk_out, (const void *)dv_out,
+                          (const void *)dstate_in})
+        if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
+    if ((rows / 64 + N + 1) * Hk > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (N == 0) return KDA_OK;
+    const size_t need = kda_gdr_backward_workspace_bytes(rows, N, Hk, H, dk, dv, dtype);
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return KDA_ERR_INVALID_ARG;
+    uint32_t *err = kda::device_error_word();
+    if (!err) return KDA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    kda::Profiler::begin(st);
+    const kda::GdrArgs a{q, k, v, g, beta, state_in, cu_seqlens, T, N, Hk, H, dk, dv,
+                         nullptr, nullptr, err, kda::next_launch_epoch()};
+    const kda::GdrGrads gr{dout, dstate_out, dq, dk_out, dv_out, dg, dbeta, dstate_in};
+    return from_cuda(kda::launch_gdr_backward(a, gr, rows, dtype == KDA_BF16, workspace, st));
+}
+
 kda_status kda_block_norm(const void *x, const void *y, const void *gate, const void *w_post,
                           const void *w_pre, int64_t rows, int width, float scale, float eps,
                           kda_dtype x_dtype, kda_dtype dtype, void *x_new, void *h,

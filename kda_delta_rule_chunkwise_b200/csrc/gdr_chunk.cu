@@ -41,6 +41,8 @@ struct ChainArgs {
     float *state_out;       // prefill
     float *n_out;           // recomputation: N [rows, H, dv]
     float *blocks;          // recomputation: state before each 64-token block [.., H, dk, dv]
+    float *tops;            // recomputation: largest |state| of each block's parts [.., H, dv/16, 2]
+    int32_t *owners;        // recomputation: the sequence of each block
     uint32_t *err;
     uint32_t epoch;
 };
@@ -95,6 +97,9 @@ __global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 
         mbar_fence_init();
         *abort = 0u;
     }
+    if (REC && h == 0 && slice == 0)
+        for (int i = threadIdx.x; 2 * i < chunks; i += blockDim.x)
+            a.owners[first_block(span, n) + i] = n;
     __syncthreads();
 
     if (warp >= NCW * KS) {
@@ -160,6 +165,9 @@ __global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 
         }
         float is0, is1;
         const float fs0 = row_scale(quad_max(m0), is0), fs1 = row_scale(quad_max(m1), is1);
+        if (REC && (ci & 1) == 0)
+            store_top(a.tops + (((first_block(span, n) + ci / 2) * a.H + h) * (a.dv / 16) + j0 / 16) * 2,
+                      fmaxf(m0, m1), KS, part);
 
         if (!warp_wait(full + st, (ci / kStages) & 1, a.err, a.epoch, abort)) return;
 
@@ -463,10 +471,20 @@ cudaError_t launch_gdr_prefill(const GdrArgs &p, cudaStream_t st) {
     using bf = __nv_bfloat16;
     gdr::ChainArgs a{(const bf *)p.q, (const bf *)p.k, (const bf *)p.v, (const bf *)p.g,
                      (const bf *)p.beta, p.state_in, p.cu_seqlens, p.T, p.Hk, p.H, p.dv,
-                     (bf *)p.o, p.state_out, nullptr, nullptr, p.err, p.epoch};
+                     (bf *)p.o, p.state_out, nullptr, nullptr, nullptr, nullptr, p.err, p.epoch};
     const int64_t units = (int64_t)p.N * p.H;
     return p.dk == 64 ? gdr::launch_chain_d<64, false>(a, units, st)
                       : gdr::launch_chain_d<128, false>(a, units, st);
+}
+
+cudaError_t launch_gdr_recompute(const GdrArgs &p, const GdrBackwardSpace &w, cudaStream_t st) {
+    using bf = __nv_bfloat16;
+    gdr::ChainArgs a{(const bf *)p.q, (const bf *)p.k, (const bf *)p.v, (const bf *)p.g,
+                     (const bf *)p.beta, p.state_in, p.cu_seqlens, p.T, p.Hk, p.H, p.dv,
+                     nullptr, nullptr, w.n, w.s_blocks, w.s_tops, w.owners, p.err, p.epoch};
+    const int64_t units = (int64_t)p.N * p.H;
+    return p.dk == 64 ? gdr::launch_chain_d<64, true>(a, units, st)
+                      : gdr::launch_chain_d<128, true>(a, units, st);
 }
 
 }  // namespace kda

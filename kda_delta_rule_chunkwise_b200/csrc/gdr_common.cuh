@@ -86,6 +86,15 @@ __device__ __forceinline__ float quad_max(float m) {
     return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
+// The largest of a warp's values (m: this lane's), for its part of a stored block: two slots,
+// one for each half of the channels (both written where one warp has them all).
+__device__ __forceinline__ void store_top(float *dst, float m, int halves, int part) {
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const int lane = threadIdx.x & 31;
+    if (halves == 2 ? lane == 0 : lane < 2) dst[halves == 2 ? part : lane] = m;
+}
+
 // Wait of a whole warp with the library's bounds: every lane takes the same way.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *err,
                                           uint32_t epoch, volatile uint32_t *abort) {

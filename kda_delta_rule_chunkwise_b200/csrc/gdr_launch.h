@@ -20,6 +20,27 @@ struct GdrArgs {
 // bf16, tensor cores
 cudaError_t launch_gdr_prefill(const GdrArgs &a, cudaStream_t st);
 
+// Backward, bf16.  Three kernels: the forward's chain again, keeping N and the state before
+// each 64-token block; the adjoint chain, keeping E and the adjoint state behind each block;
+// the gradients of each block (gdr_backward.cu).
+struct GdrBackwardSpace {
+    float *n, *e;                  // [rows, H, dv]
+    float *s_blocks, *z_blocks;    // [rows / 64 + N + 1, H, dk, dv]
+    float *s_tops, *z_tops;        // [rows / 64 + N + 1, H, dv / 16, 2]
+    int32_t *owners;               // [rows / 64 + N + 1]: a block's sequence, or -1
+};
+struct GdrGrads {
+    const void *dout;
+    const float *dstate_out;       // or nullptr
+    void *dq, *dk, *dv, *dg, *dbeta;
+    float *dstate_in;              // or nullptr
+};
+size_t gdr_backward_workspace_bytes(int64_t rows, int N, int H, int dk, int dv, bool bf16);
+cudaError_t launch_gdr_recompute(const GdrArgs &a, const GdrBackwardSpace &w, cudaStream_t st);
+// workspace: gdr_backward_workspace_bytes bytes, 256-byte aligned
+cudaError_t launch_gdr_backward(const GdrArgs &a, const GdrGrads &g, int64_t rows, bool bf16,
+                                void *workspace, cudaStream_t st);
+
 // Token by token in fp32 arithmetic (gdr_token.cu): the decode step for either type, and the
 // fp32 prefill.  State entries are slots[n] of P where given.
 struct GdrTokenArgs {
