@@ -28,6 +28,7 @@
 // orders below the tile's largest value), below the rounding of its bf16 outputs.
 #include "gdr_common.cuh"
 #include "gdr_launch.h"
+#include "gdr_token_backward.h"
 
 #include <type_traits>
 
@@ -869,6 +870,7 @@ static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t gdr_backward_workspace_bytes(int64_t rows, int N, int H, int dk, int dv, bool bf16) {
     using namespace gdr;
+    if (!bf16) return token_backward_workspace_bytes(rows, N, H, dk, dv);
     const size_t slots = (size_t)block_slots(rows, N) * H;
     return 2 * (up256((size_t)rows * H * dv * 4) + up256(slots * dk * dv * 4) + up256(slots * (dv / 8) * 4)) +
            up256(slots / H * 4);
@@ -878,6 +880,7 @@ cudaError_t launch_gdr_backward(const GdrArgs &p, const GdrGrads &g, int64_t row
                                 void *workspace, cudaStream_t st) {
     using namespace gdr;
     using bf = __nv_bfloat16;
+    if (!bf16) return launch_token_backward(p, g, rows, workspace, st);
     const size_t slots = (size_t)block_slots(rows, p.N) * p.H;
     unsigned char *w = static_cast<unsigned char *>(workspace);
     auto take = [&](size_t bytes) {

@@ -57,6 +57,37 @@ def test_decode_sizes(lib):
     assert decode(lib, N=0, P=0) == binding.KDA_OK and decode(lib, L=0) == binding.KDA_OK
 
 
+def backward(lib, **kw):
+    a = dict(q=16, k=32, v=48, g=64, beta=80, state_in=None, cu=None, B=1, T=16, N=1, Hk=2, H=4, dk=128, dv=128,
+             dtype=binding.KDA_BF16, dout=96, dstate_out=None, dq=112, dk_out=128, dv_out=144, dg=160, dbeta=176,
+             dstate_in=None, workspace=256, workspace_bytes=1 << 40, stream=None)
+    a.update(kw)
+    return lib.kda_gdr_backward(*a.values())
+
+
+@pytest.mark.parametrize("bad", [
+    dict(B=-1), dict(N=2), dict(Hk=3), dict(dtype=2), dict(q=None), dict(dout=None), dict(dq=None), dict(dk_out=None),
+    dict(dv_out=None), dict(dg=None), dict(dbeta=None), dict(dout=100), dict(dv_out=8), dict(dstate_out=4),
+    dict(workspace=None), dict(workspace=272), dict(workspace_bytes=1000)])
+def test_backward_refuses(lib, bad):
+    assert backward(lib, **bad) == BAD
+
+
+@pytest.mark.parametrize("bad", [dict(dk=96), dict(dv=256), dict(T=2 ** 31)])
+def test_backward_does_not_support(lib, bad):
+    assert backward(lib, **bad) == NOT
+
+
+def test_backward_workspace(lib):
+    f = lib.kda_gdr_backward_workspace_bytes
+    for t in (binding.KDA_BF16, binding.KDA_F32):
+        need = f(100, 2, 2, 4, 128, 64, t)
+        assert need > 0 and need % 256 == 0 and f(100, 3, 2, 4, 128, 64, t) > need
+        assert f(-1, 2, 2, 4, 128, 64, t) == 0 and f(100, 2, 3, 4, 128, 64, t) == 0 and f(100, 2, 2, 4, 96, 64, t) == 0
+        assert backward(lib, dtype=t, workspace_bytes=f(16, 1, 2, 4, 128, 128, t) - 1) == BAD
+    assert backward(lib, B=0, N=0) == binding.KDA_OK
+
+
 def test_binding_refuses_other_shapes_types_and_devices():
     q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
     v, g = torch.zeros(1, 4, 4, 64, dtype=torch.bfloat16), torch.zeros(1, 4, 4, dtype=torch.bfloat16)
