@@ -409,8 +409,9 @@ def kda_decode_step_indexed(q, k, v, g, beta, state_pool, slots, *, o=None, stre
 # ---------------------------------------------------------------- gated delta rule
 
 def _want(name, t, shape, dtype, device):
-    """Refuse a tensor of another shape, type or device than the call's."""
-    if t is None:
+    """Refuse a tensor of another shape, type or device than the call's, or a strided one."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device
+                     and t.is_contiguous()):
         return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -418,7 +419,34 @@ def _want(name, t, shape, dtype, device):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    _contig(name, t)
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _addr(t):
+    """A tensor's address as ctypes takes it for a pointer argument (None: NULL)."""
+    return None if t is None else t.data_ptr()
+
+
+class _Call:
+    """The device and stream of one call: `device` is made current for its duration where it
+    is not already, and the stream is the given one or the device's current one."""
+    __slots__ = ("index", "stream", "back")
+
+    def __init__(self, device, stream):
+        self.index = device.index
+        self.stream = (torch._C._cuda_getCurrentRawStream(self.index) if stream is None
+                       else stream.cuda_stream)
+
+    def __enter__(self):
+        now = torch._C._cuda_getDevice()
+        self.back = -1 if now == self.index else now
+        if self.back >= 0:
+            torch.cuda.set_device(self.index)
+        return self.stream
+
+    def __exit__(self, *_):
+        if self.back >= 0:
+            torch.cuda.set_device(self.back)
 
 
 def _gdr_shapes(q, k, v, g, beta):
@@ -436,11 +464,6 @@ def _gdr_shapes(q, k, v, g, beta):
                            ("beta", beta, (B, T, H))):
         _want(name, t, shape, q.dtype, q.device)
     return B, T, Hk, H, dk, dv
-
-
-def _on(device, stream):
-    """The stream of a call on `device`: the given one, or the device's current one."""
-    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
 
 
 def kda_gdr_chunk_prefill(q, k, v, g, beta, state_in=None, cu_seqlens=None, *, o=None,
@@ -464,10 +487,10 @@ def kda_gdr_chunk_prefill(q, k, v, g, beta, state_in=None, cu_seqlens=None, *, o
         o = new(v.shape, dtype=q.dtype, device=q.device)
     if state_out is None and want_state:
         state_out = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
-    with torch.cuda.device(q.device):
+    with _Call(q.device, stream) as raw_stream:
         code = load().kda_gdr_chunk_prefill(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state_in), _ptr(cu_seqlens), B, T,
-            N, Hk, H, dk, dv, _DTYPE[q.dtype], _ptr(o), _ptr(state_out), _on(q.device, stream))
+            _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(state_in), _addr(cu_seqlens), B, T,
+            N, Hk, H, dk, dv, _DTYPE[q.dtype], _addr(o), _addr(state_out), raw_stream)
     _check(code, "kda_gdr_chunk_prefill")
     return o, state_out
 
@@ -490,11 +513,11 @@ def kda_gdr_decode(q, k, v, g, beta, state, *, slots=None, lens=None, update_sta
     if o is None:
         new = torch.empty if lens is None and slots is None else torch.zeros
         o = new(v.shape, dtype=q.dtype, device=q.device)
-    with torch.cuda.device(q.device):
+    with _Call(q.device, stream) as raw_stream:
         code = load().kda_gdr_decode(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(slots), _ptr(lens), N,
-            P, L, Hk, H, dk, dv, _DTYPE[q.dtype], 1 if update_state else 0, _ptr(o),
-            _on(q.device, stream))
+            _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(state), _addr(slots), _addr(lens), N,
+            P, L, Hk, H, dk, dv, _DTYPE[q.dtype], 1 if update_state else 0, _addr(o),
+            raw_stream)
     _check(code, "kda_gdr_decode")
     return o
 
@@ -517,12 +540,12 @@ def kda_gdr_backward(q, k, v, g, beta, state_in, cu_seqlens, dout, dstate_out=No
     need = int(load().kda_gdr_backward_workspace_bytes(B * T, N, Hk, H, dk, dv, _DTYPE[q.dtype]))
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    with torch.cuda.device(q.device):
+    with _Call(q.device, stream) as raw_stream:
         code = load().kda_gdr_backward(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state_in), _ptr(cu_seqlens), B, T,
-            N, Hk, H, dk, dv, _DTYPE[q.dtype], _ptr(dout), _ptr(dstate_out), _ptr(dq), _ptr(dk_),
-            _ptr(dv_), _ptr(dg), _ptr(db), _ptr(ds0), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _on(q.device, stream))
+            _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(state_in), _addr(cu_seqlens), B, T,
+            N, Hk, H, dk, dv, _DTYPE[q.dtype], _addr(dout), _addr(dstate_out), _addr(dq), _addr(dk_),
+            _addr(dv_), _addr(dg), _addr(db), _addr(ds0), _addr(workspace),
+            workspace.numel() * workspace.element_size(), raw_stream)
     _check(code, "kda_gdr_backward")
     return dq, dk_, dv_, dg, db, ds0
 
@@ -585,11 +608,11 @@ def kda_block_norm(x, y, gate, w_post, w_pre, *, scale=1.0, eps=1e-6, x_new=None
     _want("h", h, y.shape, y.dtype, x.device)
     x_new = torch.empty_like(x) if x_new is None else x_new
     h = torch.empty_like(y) if h is None else h
-    with torch.cuda.device(x.device):
+    with _Call(x.device, stream) as raw_stream:
         code = load().kda_block_norm(
-            _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(w_pre), rows, D, float(scale),
-            float(eps), _DTYPE[x.dtype], _DTYPE[y.dtype], _ptr(x_new), _ptr(h),
-            _on(x.device, stream))
+            _addr(x), _addr(y), _addr(gate), _addr(w_post), _addr(w_pre), rows, D, float(scale),
+            float(eps), _DTYPE[x.dtype], _DTYPE[y.dtype], _addr(x_new), _addr(h),
+            raw_stream)
     _check(code, "kda_block_norm")
     return x_new, h
 
@@ -610,11 +633,11 @@ def kda_block_norm_backward(x, y, gate, w_post, w_pre, dx_new, dh, *, scale=1.0,
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with torch.cuda.device(x.device):
+    with _Call(x.device, stream) as raw_stream:
         code = load().kda_block_norm_backward(
-            _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(dx_new), _ptr(dh), rows,
-            D, float(scale), float(eps), _DTYPE[x.dtype], _DTYPE[y.dtype], _ptr(dx), _ptr(dy),
-            _ptr(dgate), _ptr(dw[0]), _ptr(dw[1]), _ptr(workspace), ws_bytes, _on(x.device, stream))
+            _addr(x), _addr(y), _addr(gate), _addr(w_post), _addr(w_pre), _addr(dx_new), _addr(dh), rows,
+            D, float(scale), float(eps), _DTYPE[x.dtype], _DTYPE[y.dtype], _addr(dx), _addr(dy),
+            _addr(dgate), _addr(dw[0]), _addr(dw[1]), _addr(workspace), ws_bytes, raw_stream)
     _check(code, "kda_block_norm_backward")
     return dx, dy, dgate, dw[0], dw[1]
 

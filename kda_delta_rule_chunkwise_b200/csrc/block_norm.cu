@@ -21,30 +21,43 @@
 namespace kda {
 namespace {
 
-template <int V> struct Floats { float v[V]; };
-
+// V consecutive elements as loaded: 16 bytes of bf16, 32 of fp32, or one element.  They stay
+// packed in registers and are widened where they are used.
 template <int V, typename T>
-__device__ __forceinline__ Floats<V> load(const T *p) {
-    Floats<V> r;
-    if constexpr (V == 1) {
-        r.v[0] = to_f32(*p);
-    } else if constexpr (sizeof(T) == 2) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Pack {
+    static constexpr int WORDS = V == 1 ? 1 : V * (int)sizeof(T) / 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (V == 1) {
+            w[0] = __float_as_uint(to_f32(*p));
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            r.v[2 * i] = __uint_as_float(u[i] << 16);
-            r.v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 w = reinterpret_cast<const float4 *>(p)[i];
-            r.v[4 * i] = w.x; r.v[4 * i + 1] = w.y; r.v[4 * i + 2] = w.z; r.v[4 * i + 3] = w.w;
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+            }
         }
     }
-    return r;
-}
+    __device__ __forceinline__ void load_shared(const T *p) {   // weights: read by every row
+        if constexpr (V == 1) {
+            w[0] = __float_as_uint(to_f32(__ldg(p)));
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ float get(int j) const {
+        if constexpr (V == 1 || sizeof(T) == 4) return __uint_as_float(w[j]);
+        else return __uint_as_float((j & 1) ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    }
+};
 
 template <int V, typename T>
 __device__ __forceinline__ void store(T *p, const float (&x)[V]) {
@@ -57,184 +70,201 @@ __device__ __forceinline__ void store(T *p, const float (&x)[V]) {
             const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
             u[i] = reinterpret_cast<const uint32_t &>(b);
         }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+        __stcs(reinterpret_cast<uint4 *>(p), make_uint4(u[0], u[1], u[2], u[3]));
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            reinterpret_cast<float4 *>(p)[i] =
-                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            __stcs(reinterpret_cast<float4 *>(p) + i,
+                   make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
     }
 }
 
-// Sum over the TPR threads of a row, the same bits in each: within a warp by shuffles,
-// across warps through shared memory (then the CTA is one row).  `red` is a slot of its own
-// for each call between two barriers.
+// Sums of x and y over the TPR threads of a row, the same bits in each: within a warp by
+// shuffles, across warps through shared memory (then the CTA is one row).  `red` is a slot of
+// its own for each call between two barriers.
 template <int TPR>
-__device__ __forceinline__ float row_sum(float x, float *red) {
+__device__ __forceinline__ float2 row_sum(float x, float y, float2 *red) {
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-    if constexpr (TPR > 32) {
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-        __syncthreads();
-        x = 0.f;
-#pragma unroll
-        for (int w = 0; w < TPR / 32; ++w) x += red[w];
+    for (int m = 16; m > 0; m >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, m);
+        y += __shfl_xor_sync(0xffffffffu, y, m);
     }
-    return x;
+    if constexpr (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(x, y);
+        __syncthreads();
+        x = y = 0.f;
+#pragma unroll
+        for (int w = 0; w < TPR / 32; ++w) {
+            const float2 v = red[w];
+            x += v.x;
+            y += v.y;
+        }
+    }
+    return make_float2(x, y);
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 // V elements per vector, NV vectors per thread, TPR threads per row.
 template <int V, int NV, int TPR, typename TX, typename T>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) block_norm_kernel(BlockNormArgs a) {
     constexpr int RPC = TPR > 32 ? 1 : 8;   // rows per CTA
-    __shared__ float red[2][TPR / 32];
+    __shared__ float2 red[2][TPR / 32];
     const int t = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * RPC + threadIdx.x / TPR;
     if (RPC > 1 && row >= a.rows) return;   // a whole warp
     const int D = a.width;
-    const TX *x = (const TX *)a.x + row * D;
-    const T *y = (const T *)a.y + row * D, *gate = (const T *)a.gate;
-    if (gate) gate += row * D;
+    const int64_t at = row * D;
+    const bool gated = a.gate != nullptr;
 
-    Floats<V> xv[NV], yv[NV], gv[NV];
-    float ss = 0.f;
+    Pack<V, TX> x[NV];
+    Pack<V, T> y[NV], g[NV], wo[NV], wi[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + t) * V;
+        y[i].zero();
         if (c < D) {
-            yv[i] = load<V>(y + c);
-            xv[i] = load<V>(x + c);
-            if (gate) gv[i] = load<V>(gate + c);
+            y[i].load((const T *)a.y + at + c);
+            x[i].load((const TX *)a.x + at + c);
+            if (gated) g[i].load((const T *)a.gate + at + c);
+            wo[i].load_shared((const T *)a.w_post + c);
+            wi[i].load_shared((const T *)a.w_pre + c);
         }
     }
+    float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if ((i * TPR + t) * V < D)
 #pragma unroll
-            for (int j = 0; j < V; ++j) ss = fmaf(yv[i].v[j], yv[i].v[j], ss);
-    const float ry = rsqrtf(row_sum<TPR>(ss, red[0]) / D + a.eps) * a.scale;
+        for (int j = 0; j < V; ++j) ss = fmaf(y[i].get(j), y[i].get(j), ss);
+    const float ry = rsqrtf(row_sum<TPR>(ss, 0.f, red[0]).x / D + a.eps) * a.scale;
+    float xn[NV][V];
     ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + t) * V;
         if (c >= D) continue;
-        const Floats<V> w = load<V>((const T *)a.w_post + c);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float g = gate ? sigmoid(gv[i].v[j]) : 1.f;
-            xv[i].v[j] = fmaf(yv[i].v[j] * ry * w.v[j], g, xv[i].v[j]);
-            ss = fmaf(xv[i].v[j], xv[i].v[j], ss);
+            const float s = gated ? sigmoid(g[i].get(j)) : 1.f;
+            xn[i][j] = fmaf(y[i].get(j) * ry * wo[i].get(j), s, x[i].get(j));
+            ss = fmaf(xn[i][j], xn[i][j], ss);
         }
-        store<V>((TX *)a.x_new + row * D + c, xv[i].v);
+        store<V>((TX *)a.x_new + at + c, xn[i]);
     }
-    const float rx = rsqrtf(row_sum<TPR>(ss, red[1]) / D + a.eps);
+    const float rx = rsqrtf(row_sum<TPR>(ss, 0.f, red[1]).x / D + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + t) * V;
         if (c >= D) continue;
-        const Floats<V> w = load<V>((const T *)a.w_pre + c);
         float h[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) h[j] = xv[i].v[j] * rx * w.v[j];
-        store<V>((T *)a.h + row * D + c, h);
+        for (int j = 0; j < V; ++j) h[j] = xn[i][j] * rx * wi[i].get(j);
+        store<V>((T *)a.h + at + c, h);
     }
 }
 
-// A CTA walks rows blockIdx.x RPC + k gridDim.x RPC; its sums of the weight gradients go to
-// part[cta][2][D] (with several rows side by side, to part[cta * RPC + side]).
+// A row's inputs to the backward, as loaded.
 template <int V, int NV, int TPR, typename TX, typename T>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) block_norm_backward_kernel(BlockNormArgs a) {
+struct BackwardRow {
+    Pack<V, TX> x[NV], dx[NV];
+    Pack<V, T> y[NV], g[NV], dh[NV];
+    __device__ __forceinline__ void load(const BlockNormArgs &a, int64_t row, int t) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * V;
+            const int64_t at = row * a.width + c;
+            x[i].zero(); dx[i].zero(); y[i].zero(); g[i].zero(); dh[i].zero();
+            if (row < a.rows && c < a.width) {
+                y[i].load((const T *)a.y + at);
+                x[i].load((const TX *)a.x + at);
+                if (a.gate) g[i].load((const T *)a.gate + at);
+                if (a.dh) dh[i].load((const T *)a.dh + at);
+                if (a.dx_new) dx[i].load((const TX *)a.dx_new + at);
+            }
+        }
+    }
+};
+
+// A CTA walks rows blockIdx.x RPC + k gridDim.x RPC; the next row is on its way while one is
+// worked on.  Its sums of the weight gradients go to part[cta][2][D] (with several rows side by
+// side, to part[cta RPC + side]).
+template <int V, int NV, int TPR, typename TX, typename T>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256, TPR > 256 ? 1 : 2)
+    block_norm_backward_kernel(BlockNormArgs a) {
     constexpr int RPC = TPR > 32 ? 1 : 8;
-    __shared__ float red[2][4][TPR / 32];
+    __shared__ float2 red[2][3][TPR / 32];
     const int t = threadIdx.x % TPR, side = threadIdx.x / TPR;
     const int D = a.width;
-    const T *gate = (const T *)a.gate;
+    const bool gated = a.gate != nullptr;
     const float inv_d = 1.f / D;
-    float wo[NV][V], wi[NV][V];
+    float dwo[NV][V], dwi[NV][V];
+    Pack<V, T> wo[NV], wi[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        wo[i].zero(), wi[i].zero();
+        if ((i * TPR + t) * V < D) {
+            wo[i].load_shared((const T *)a.w_post + (i * TPR + t) * V);
+            wi[i].load_shared((const T *)a.w_pre + (i * TPR + t) * V);
+        }
 #pragma unroll
-        for (int j = 0; j < V; ++j) wo[i][j] = wi[i][j] = 0.f;
+        for (int j = 0; j < V; ++j) dwo[i][j] = dwi[i][j] = 0.f;
+    }
+    BackwardRow<V, NV, TPR, TX, T> next;
+    const int64_t first = (int64_t)blockIdx.x * RPC + side, step = (int64_t)gridDim.x * RPC;
+    next.load(a, first, t);
     int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * RPC + side; row < a.rows;
-         row += (int64_t)gridDim.x * RPC, turn ^= 1) {
+    for (int64_t row = first; row < a.rows; row += step, turn ^= 1) {
+        const BackwardRow<V, NV, TPR, TX, T> in = next;
+        next.load(a, row + step, t);
         const int64_t at = row * D;
-        Floats<V> xv[NV], yv[NV], gv[NV], hv[NV], dv[NV];
         float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + t) * V;
-            if (c >= D) continue;
-            yv[i] = load<V>((const T *)a.y + at + c);
-            xv[i] = load<V>((const TX *)a.x + at + c);
-            if (gate) gv[i] = load<V>(gate + at + c);
-            if (a.dh) hv[i] = load<V>((const T *)a.dh + at + c);
-            if (a.dx_new) dv[i] = load<V>((const TX *)a.dx_new + at + c);
-        }
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if ((i * TPR + t) * V >= D) continue;
+            for (int j = 0; j < V; ++j) ss = fmaf(in.y[i].get(j), in.y[i].get(j), ss);
+        const float ry = rsqrtf(row_sum<TPR>(ss, 0.f, red[turn][0]).x / D + a.eps);
+        // x' and the gate; the two sums of the second norm
+        float xn[NV][V], s[NV][V], sx = 0.f, sg = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                gv[i].v[j] = gate ? sigmoid(gv[i].v[j]) : 1.f;
-                if (!a.dh) hv[i].v[j] = 0.f;
-                if (!a.dx_new) dv[i].v[j] = 0.f;
-                ss = fmaf(yv[i].v[j], yv[i].v[j], ss);
+                s[i][j] = gated ? sigmoid(in.g[i].get(j)) : 1.f;
+                xn[i][j] = fmaf(in.y[i].get(j) * ry * wo[i].get(j), a.scale * s[i][j], in.x[i].get(j));
+                sx = fmaf(xn[i][j], xn[i][j], sx);
+                sg = fmaf(in.dh[i].get(j) * wi[i].get(j), xn[i][j], sg);
             }
-        }
-        const float ry = rsqrtf(row_sum<TPR>(ss, red[turn][0]) / D + a.eps);
-        // x' in place of x; the two sums of the second norm
-        float sx = 0.f, sg = 0.f;
+        const float2 two = row_sum<TPR>(sx, sg, red[turn][1]);
+        const float rx = rsqrtf(two.x / D + a.eps), kx = rx * rx * rx * (two.y * inv_d);
+        float gy[NV][V], sy = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * V;
-            if (c >= D) continue;
-            const Floats<V> w = load<V>((const T *)a.w_post + c), u = load<V>((const T *)a.w_pre + c);
+            float dx[V], dg[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float s = a.scale * gv[i].v[j];
-                xv[i].v[j] = fmaf(yv[i].v[j] * ry * w.v[j], s, xv[i].v[j]);
-                sx = fmaf(xv[i].v[j], xv[i].v[j], sx);
-                sg = fmaf(hv[i].v[j] * u.v[j], xv[i].v[j], sg);
+                const float h = in.dh[i].get(j), yn = in.y[i].get(j) * ry;
+                dwi[i][j] = fmaf(h, xn[i][j] * rx, dwi[i][j]);
+                dx[j] = in.dx[i].get(j) + rx * (h * wi[i].get(j)) - kx * xn[i][j];
+                const float dn = a.scale * dx[j] * s[i][j];
+                dg[j] = dn * (1.f - s[i][j]) * (yn * wo[i].get(j));
+                dwo[i][j] = fmaf(dn, yn, dwo[i][j]);
+                gy[i][j] = dn * wo[i].get(j);
+                sy = fmaf(gy[i][j], in.y[i].get(j), sy);
+            }
+            if (c < D) {
+                store<V>((TX *)a.dx + at + c, dx);
+                if (gated) store<V>((T *)a.dgate + at + c, dg);
             }
         }
-        sx = row_sum<TPR>(sx, red[turn][1]);
-        sg = row_sum<TPR>(sg, red[turn][2]);
-        const float rx = rsqrtf(sx / D + a.eps), kx = rx * rx * rx * (sg * inv_d);
-        float sy = 0.f;
+        const float ky = ry * ry * ry * (row_sum<TPR>(sy, 0.f, red[turn][2]).x * inv_d);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * V;
-            if (c >= D) continue;
-            const Floats<V> w = load<V>((const T *)a.w_post + c), u = load<V>((const T *)a.w_pre + c);
-            float dg[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                wi[i][j] = fmaf(hv[i].v[j], xv[i].v[j] * rx, wi[i][j]);
-                const float d = dv[i].v[j] + rx * (hv[i].v[j] * u.v[j]) - kx * xv[i].v[j];
-                dv[i].v[j] = d;                              // dx
-                const float s = a.scale * d, yn = yv[i].v[j] * ry, g = gv[i].v[j];
-                const float dn = s * g;
-                dg[j] = dn * (1.f - g) * (yn * w.v[j]);
-                wo[i][j] = fmaf(dn, yn, wo[i][j]);
-                hv[i].v[j] = dn * w.v[j];                    // gy
-                sy = fmaf(hv[i].v[j], yv[i].v[j], sy);
-            }
-            store<V>((TX *)a.dx + at + c, dv[i].v);
-            if (gate) store<V>((T *)a.dgate + at + c, dg);
-        }
-        sy = row_sum<TPR>(sy, red[turn][3]);
-        const float ky = ry * ry * ry * (sy * inv_d);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + t) * V;
-            if (c >= D) continue;
             float d[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) d[j] = fmaf(ry, hv[i].v[j], -ky * yv[i].v[j]);
-            store<V>((T *)a.dy + at + c, d);
+            for (int j = 0; j < V; ++j) d[j] = fmaf(ry, gy[i][j], -ky * in.y[i].get(j));
+            if (c < D) store<V>((T *)a.dy + at + c, d);
         }
     }
     float *part = a.part + ((int64_t)blockIdx.x * RPC + side) * 2 * D;
@@ -244,8 +274,8 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) block_norm_backward_ker
         if (c >= D) continue;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            part[c + j] = wo[i][j];
-            part[D + c + j] = wi[i][j];
+            part[c + j] = dwo[i][j];
+            part[D + c + j] = dwi[i][j];
         }
     }
 }
@@ -299,8 +329,8 @@ cudaError_t launch_t(BlockNormArgs a, bool backward, cudaStream_t st) {
     return e;
 }
 
-// Threads per row: two vectors a thread from 512 vectors on, one below (a row's latency then
-// counts more than the number of its threads).
+// Threads per row: one vector a thread up to 512 of them; a row's values and the next one's
+// then fit the registers in either direction.
 template <int V, typename TX, typename T>
 cudaError_t launch_v(const BlockNormArgs &a, bool b, cudaStream_t st) {
     const int vecs = (a.width + V - 1) / V;
@@ -308,13 +338,13 @@ cudaError_t launch_v(const BlockNormArgs &a, bool b, cudaStream_t st) {
     if (vecs <= 64) return launch_t<V, 1, 64, TX, T>(a, b, st);
     if (vecs <= 128) return launch_t<V, 1, 128, TX, T>(a, b, st);
     if (vecs <= 256) return launch_t<V, 1, 256, TX, T>(a, b, st);
-    if (vecs <= 512) return launch_t<V, 2, 256, TX, T>(a, b, st);
+    if (vecs <= 512) return launch_t<V, 1, 512, TX, T>(a, b, st);
     if (vecs <= 1024) return launch_t<V, 2, 512, TX, T>(a, b, st);
     if constexpr (V == 8) {
-        return launch_t<V, 2, 1024, TX, T>(a, b, st);
+        return launch_t<V, 4, 512, TX, T>(a, b, st);
     } else {
         if (vecs <= 4096) return launch_t<V, 8, 512, TX, T>(a, b, st);
-        return launch_t<V, 16, 1024, TX, T>(a, b, st);
+        return launch_t<V, 32, 512, TX, T>(a, b, st);
     }
 }
 
