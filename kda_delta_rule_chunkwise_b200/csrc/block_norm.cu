@@ -18,6 +18,8 @@
 #include "block_norm.h"
 #include "kda_common.cuh"
 
+#include <type_traits>
+
 namespace kda {
 namespace {
 
@@ -47,6 +49,15 @@ struct Pack {
                 const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i);
                 w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
             }
+        }
+    }
+    __device__ __forceinline__ void load_staged(const unsigned char *tile, int c) {   // V > 1
+        const uint4 *p = reinterpret_cast<const uint4 *>(tile + (size_t)c * sizeof(T));
+#pragma unroll
+        for (int i = 0; i < (WORDS + 3) / 4; ++i) {
+            const uint4 u = p[i];
+            w[4 * i] = u.x;
+            if constexpr (WORDS > 1) { w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w; }
         }
     }
     __device__ __forceinline__ void zero() {
@@ -79,25 +90,41 @@ __device__ __forceinline__ void store(T *p, const float (&x)[V]) {
     }
 }
 
-// Sums of x and y over the TPR threads of a row, the same bits in each: within a warp by
-// shuffles, across warps through shared memory (then the CTA is one row).  `red` is a slot of
+// Sums of x over the TPR threads of a row, the same bits in each: within a warp by shuffles,
+// across warps through shared memory.  Every thread of the CTA takes part.  `red` is a slot of
 // its own for each call between two barriers.
 template <int TPR>
-__device__ __forceinline__ float2 row_sum(float x, float y, float2 *red) {
+__device__ __forceinline__ float row_sum(float x, float *red) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    constexpr int NW = TPR / 32;   // warps of a row
+    if (NW > 1 && (threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    if constexpr (NW > 1) {
+        x = red[threadIdx.x / TPR * NW + (threadIdx.x & (NW - 1))];
+#pragma unroll
+        for (int m = NW / 2; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    }
+    return x;
+}
+// The same of two sums at once.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum2(float x, float y, float2 *red) {
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
         x += __shfl_xor_sync(0xffffffffu, x, m);
         y += __shfl_xor_sync(0xffffffffu, y, m);
     }
-    if constexpr (TPR > 32) {
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(x, y);
-        __syncthreads();
-        x = y = 0.f;
+    constexpr int NW = TPR / 32;
+    if (NW > 1 && (threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(x, y);
+    __syncthreads();
+    if constexpr (NW > 1) {
+        const float2 v = red[threadIdx.x / TPR * NW + (threadIdx.x & (NW - 1))];
+        x = v.x, y = v.y;
 #pragma unroll
-        for (int w = 0; w < TPR / 32; ++w) {
-            const float2 v = red[w];
-            x += v.x;
-            y += v.y;
+        for (int m = NW / 2; m > 0; m >>= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, m);
+            y += __shfl_xor_sync(0xffffffffu, y, m);
         }
     }
     return make_float2(x, y);
@@ -105,98 +132,207 @@ __device__ __forceinline__ float2 row_sum(float x, float y, float2 *red) {
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
-// V elements per vector, NV vectors per thread, TPR threads per row.
-template <int V, int NV, int TPR, typename TX, typename T>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) block_norm_kernel(BlockNormArgs a) {
-    constexpr int RPC = TPR > 32 ? 1 : 8;   // rows per CTA
-    __shared__ float2 red[2][TPR / 32];
-    const int t = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * RPC + threadIdx.x / TPR;
-    if (RPC > 1 && row >= a.rows) return;   // a whole warp
-    const int D = a.width;
-    const int64_t at = row * D;
-    const bool gated = a.gate != nullptr;
 
-    Pack<V, TX> x[NV];
-    Pack<V, T> y[NV], g[NV], wo[NV], wi[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + t) * V;
-        y[i].zero();
-        if (c < D) {
-            y[i].load((const T *)a.y + at + c);
-            x[i].load((const TX *)a.x + at + c);
-            if (gated) g[i].load((const T *)a.gate + at + c);
-            wo[i].load_shared((const T *)a.w_post + c);
-            wi[i].load_shared((const T *)a.w_pre + c);
-        }
-    }
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) ss = fmaf(y[i].get(j), y[i].get(j), ss);
-    const float ry = rsqrtf(row_sum<TPR>(ss, 0.f, red[0]).x / D + a.eps) * a.scale;
-    float xn[NV][V];
-    ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + t) * V;
-        if (c >= D) continue;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float s = gated ? sigmoid(g[i].get(j)) : 1.f;
-            xn[i][j] = fmaf(y[i].get(j) * ry * wo[i].get(j), s, x[i].get(j));
-            ss = fmaf(xn[i][j], xn[i][j], ss);
-        }
-        store<V>((TX *)a.x_new + at + c, xn[i]);
-    }
-    const float rx = rsqrtf(row_sum<TPR>(ss, 0.f, red[1]).x / D + a.eps);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + t) * V;
-        if (c >= D) continue;
-        float h[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[j] = xn[i][j] * rx * wi[i].get(j);
-        store<V>((T *)a.h + at + c, h);
-    }
-}
+// The inputs of the rows that a CTA works on: NT / TPR rows side by side, TPR threads and NV
+// vectors of V elements each.  STAGED: they come through a ring of `stages` row groups in
+// shared memory, each filled by one bulk copy per tensor (the rows of a group are contiguous),
+// so that as many bytes are in flight as the ring holds; a stage is filled again as soon as the
+// first barrier after its reading has passed, each tensor's copy issued by a warp of its own.
+// Otherwise (widths or addresses that are no multiple of 16 bytes, rows too wide for the ring)
+// each thread loads its own elements.
+template <int V, int NV, int TPR, int NT, bool BACK, bool STAGED, typename TX, typename T>
+struct RowSource {
+    static constexpr int RPC = NT / TPR;
+    Pack<V, TX> x[NV], dx[BACK ? NV : 1];
+    Pack<V, T> y[NV], g[NV], dh[BACK ? NV : 1];
 
-// A row's inputs to the backward, as loaded.
-template <int V, int NV, int TPR, typename TX, typename T>
-struct BackwardRow {
-    Pack<V, TX> x[NV], dx[NV];
-    Pack<V, T> y[NV], g[NV], dh[NV];
-    __device__ __forceinline__ void load(const BlockNormArgs &a, int64_t row, int t) {
+    static __device__ __forceinline__ uint32_t stage_bytes(const BlockNormArgs &a) {
+        return (uint32_t)RPC * a.width *
+               ((BACK ? 2 : 1) * sizeof(TX) + ((BACK ? 2 : 1) + (a.gate ? 1 : 0)) * sizeof(T));
+    }
+    // What this thread copies for each group: lane 0 of warp w has tensor w of y, x, gate, dh,
+    // dx_new (`bytes` per row, 0: none), and warp 0's also announces all tensors' bytes.
+    struct Copier {
+        const unsigned char *src;
+        uint32_t bytes, offset, total;
+    };
+    static __device__ __forceinline__ Copier copier(const BlockNormArgs &a) {
+        Copier c{nullptr, 0u, 0u, 0u};
+        if (threadIdx.x & 31) return c;
+        const int w = threadIdx.x >> 5;
+        uint32_t offset = 0;
+        auto tensor = [&](int i, const void *p, uint32_t el, bool room) {
+            if (p) {
+                if (i == w) c.src = (const unsigned char *)p, c.bytes = a.width * el, c.offset = offset;
+                if (w == 0) c.total += a.width * el;
+            }
+            if (room) offset += RPC * a.width * el;
+        };
+        tensor(0, a.y, sizeof(T), true);
+        tensor(1, a.x, sizeof(TX), true);
+        tensor(2, a.gate, sizeof(T), a.gate != nullptr);
+        if (BACK) {
+            tensor(3, a.dh, sizeof(T), true);
+            tensor(4, a.dx_new, sizeof(TX), true);
+        }
+        return c;
+    }
+    // the group of rows from `row` into the stage `dst` of barrier `bar`
+    static __device__ __forceinline__ void issue(const BlockNormArgs &a, const Copier &c, int row,
+                                                 uint32_t dst, uint64_t *bar) {
+        if (c.bytes == 0 || row >= a.rows) return;
+        const uint32_t n = min((int)a.rows - row, RPC);
+        if (c.total) mbar_arrive_expect_tx(bar, n * c.total);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+                "r"(dst + c.offset), "l"(c.src + (int64_t)row * c.bytes), "r"(n * c.bytes), "r"(smem_u32(bar))
+            : "memory");
+    }
+    // this thread's elements of its row of the group, from the stage `tile` if STAGED
+    __device__ __forceinline__ void read(const BlockNormArgs &a, int row, const unsigned char *tile) {
+        const int t = threadIdx.x % TPR, side = threadIdx.x / TPR;
+        const bool live = row < a.rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * V;
-            const int64_t at = row * a.width + c;
-            x[i].zero(); dx[i].zero(); y[i].zero(); g[i].zero(); dh[i].zero();
-            if (row < a.rows && c < a.width) {
+            y[i].zero(), x[i].zero(), g[i].zero();
+            if (BACK) dh[i].zero(), dx[i].zero();
+            if (!live || c >= a.width) continue;
+            if constexpr (STAGED) {
+                const unsigned char *p = tile;
+                const int at = side * a.width + c;
+                const uint32_t row_group = (uint32_t)RPC * a.width;
+                y[i].load_staged(p, at);
+                p += row_group * sizeof(T);
+                x[i].load_staged(p, at);
+                p += row_group * sizeof(TX);
+                if (a.gate) {
+                    g[i].load_staged(p, at);
+                    p += row_group * sizeof(T);
+                }
+                if (BACK) {
+                    if (a.dh) dh[i].load_staged(p, at);
+                    p += row_group * sizeof(T);
+                    if (a.dx_new) dx[i].load_staged(p, at);
+                }
+            } else {
+                const int64_t at = (int64_t)row * a.width + c;
                 y[i].load((const T *)a.y + at);
                 x[i].load((const TX *)a.x + at);
                 if (a.gate) g[i].load((const T *)a.gate + at);
-                if (a.dh) dh[i].load((const T *)a.dh + at);
-                if (a.dx_new) dx[i].load((const TX *)a.dx_new + at);
+                if (BACK) {
+                    if (a.dh) dh[i].load((const T *)a.dh + at);
+                    if (a.dx_new) dx[i].load((const TX *)a.dx_new + at);
+                }
             }
         }
     }
 };
 
-// A CTA walks rows blockIdx.x RPC + k gridDim.x RPC; the next row is on its way while one is
-// worked on.  Its sums of the weight gradients go to part[cta][2][D] (with several rows side by
-// side, to part[cta RPC + side]).
-template <int V, int NV, int TPR, typename TX, typename T>
-__global__ void __launch_bounds__(TPR > 256 ? TPR : 256, TPR > 256 ? 1 : 2)
-    block_norm_backward_kernel(BlockNormArgs a) {
-    constexpr int RPC = TPR > 32 ? 1 : 8;
-    __shared__ float2 red[2][3][TPR / 32];
+template <int V, int NV, int TPR, int NT, int CTAS, bool STAGED, typename TX, typename T>
+__global__ void __launch_bounds__(NT, CTAS) block_norm_kernel(BlockNormArgs a) {
+    using Rows = RowSource<V, NV, TPR, NT, false, STAGED, TX, T>;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ float red[2][2][NT / 32];
+    __shared__ uint64_t bars[kBlockNormStages];
+    __shared__ volatile uint32_t abort;
+    const int t = threadIdx.x % TPR, side = threadIdx.x / TPR;
+    const int D = a.width;
+    const bool gated = a.gate != nullptr;
+    const auto copier = Rows::copier(a);
+    const int first = blockIdx.x * Rows::RPC, step = gridDim.x * Rows::RPC;   // rows of a group
+    const uint32_t bytes = STAGED ? Rows::stage_bytes(a) : 0u, ring_at = smem_u32(ring);
+    if (STAGED) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < kBlockNormStages; ++i) mbar_init(bars + i, 1);
+            mbar_fence_init();
+            abort = 0u;
+        }
+        __syncthreads();
+        for (int i = 0; i < a.stages; ++i)
+            if (first + (int64_t)i * step < a.rows)
+                Rows::issue(a, copier, first + i * step, ring_at + i * bytes, bars + i);
+    }
+    Pack<V, T> wo[NV], wi[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        wo[i].zero(), wi[i].zero();
+        if ((i * TPR + t) * V < D) {
+            wo[i].load_shared((const T *)a.w_post + (i * TPR + t) * V);
+            wi[i].load_shared((const T *)a.w_pre + (i * TPR + t) * V);
+        }
+    }
+    int stage = 0, turn = 0;
+    uint32_t parity = 0;
+    for (int64_t base = first; base < a.rows; base += step, turn ^= 1) {
+        Rows in;
+        const int row = (int)base + side;
+        const int64_t at = (int64_t)row * D;
+        if (STAGED && !mbar_wait_abortable(bars + stage, parity, a.err, a.epoch, &abort)) return;
+        in.read(a, row, ring + stage * bytes);
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) ss = fmaf(in.y[i].get(j), in.y[i].get(j), ss);
+        const float ry = rsqrtf(row_sum<TPR>(ss, red[turn][0]) / D + a.eps) * a.scale;
+        if (STAGED) {
+            if (base + (int64_t)a.stages * step < a.rows)
+                Rows::issue(a, copier, (int)base + a.stages * step, ring_at + stage * bytes, bars + stage);
+            if (++stage == a.stages) stage = 0, parity ^= 1u;
+        }
+        float xn[NV][V];
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float s = gated ? sigmoid(in.g[i].get(j)) : 1.f;
+                xn[i][j] = fmaf(in.y[i].get(j) * ry * wo[i].get(j), s, in.x[i].get(j));
+                ss = fmaf(xn[i][j], xn[i][j], ss);
+            }
+            if (row < a.rows && c < D) store<V>((TX *)a.x_new + at + c, xn[i]);
+        }
+        const float rx = rsqrtf(row_sum<TPR>(ss, red[turn][1]) / D + a.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * V;
+            float h[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) h[j] = xn[i][j] * rx * wi[i].get(j);
+            if (row < a.rows && c < D) store<V>((T *)a.h + at + c, h);
+        }
+    }
+}
+
+// The sums of the weight gradients over a CTA's rows go to part[cta RPC + side][2][D].
+template <int V, int NV, int TPR, int NT, int CTAS, bool STAGED, typename TX, typename T>
+__global__ void __launch_bounds__(NT, CTAS) block_norm_backward_kernel(BlockNormArgs a) {
+    using Rows = RowSource<V, NV, TPR, NT, true, STAGED, TX, T>;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ float red[2][2][NT / 32];
+    __shared__ float2 red2[2][NT / 32];
+    __shared__ uint64_t bars[kBlockNormStages];
+    __shared__ volatile uint32_t abort;
     const int t = threadIdx.x % TPR, side = threadIdx.x / TPR;
     const int D = a.width;
     const bool gated = a.gate != nullptr;
     const float inv_d = 1.f / D;
+    const auto copier = Rows::copier(a);
+    const int first = blockIdx.x * Rows::RPC, step = gridDim.x * Rows::RPC;   // rows of a group
+    const uint32_t bytes = STAGED ? Rows::stage_bytes(a) : 0u, ring_at = smem_u32(ring);
+    if (STAGED) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < kBlockNormStages; ++i) mbar_init(bars + i, 1);
+            mbar_fence_init();
+            abort = 0u;
+        }
+        __syncthreads();
+        for (int i = 0; i < a.stages; ++i)
+            if (first + (int64_t)i * step < a.rows)
+                Rows::issue(a, copier, first + i * step, ring_at + i * bytes, bars + i);
+    }
     float dwo[NV][V], dwi[NV][V];
     Pack<V, T> wo[NV], wi[NV];
 #pragma unroll
@@ -209,20 +345,26 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256, TPR > 256 ? 1 : 2)
 #pragma unroll
         for (int j = 0; j < V; ++j) dwo[i][j] = dwi[i][j] = 0.f;
     }
-    BackwardRow<V, NV, TPR, TX, T> next;
-    const int64_t first = (int64_t)blockIdx.x * RPC + side, step = (int64_t)gridDim.x * RPC;
-    next.load(a, first, t);
-    int turn = 0;
-    for (int64_t row = first; row < a.rows; row += step, turn ^= 1) {
-        const BackwardRow<V, NV, TPR, TX, T> in = next;
-        next.load(a, row + step, t);
-        const int64_t at = row * D;
+    int stage = 0, turn = 0;
+    uint32_t parity = 0;
+    for (int64_t base = first; base < a.rows; base += step, turn ^= 1) {
+        Rows in;
+        const int row = (int)base + side;
+        const int64_t at = (int64_t)row * D;
+        if (STAGED && !mbar_wait_abortable(bars + stage, parity, a.err, a.epoch, &abort)) return;
+        in.read(a, row, ring + stage * bytes);
+        const bool live = row < a.rows;
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) ss = fmaf(in.y[i].get(j), in.y[i].get(j), ss);
-        const float ry = rsqrtf(row_sum<TPR>(ss, 0.f, red[turn][0]).x / D + a.eps);
+        const float ry = rsqrtf(row_sum<TPR>(ss, red[turn][0]) / D + a.eps);
+        if (STAGED) {
+            if (base + (int64_t)a.stages * step < a.rows)
+                Rows::issue(a, copier, (int)base + a.stages * step, ring_at + stage * bytes, bars + stage);
+            if (++stage == a.stages) stage = 0, parity ^= 1u;
+        }
         // x' and the gate; the two sums of the second norm
         float xn[NV][V], s[NV][V], sx = 0.f, sg = 0.f;
 #pragma unroll
@@ -234,7 +376,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256, TPR > 256 ? 1 : 2)
                 sx = fmaf(xn[i][j], xn[i][j], sx);
                 sg = fmaf(in.dh[i].get(j) * wi[i].get(j), xn[i][j], sg);
             }
-        const float2 two = row_sum<TPR>(sx, sg, red[turn][1]);
+        const float2 two = row_sum2<TPR>(sx, sg, red2[turn]);
         const float rx = rsqrtf(two.x / D + a.eps), kx = rx * rx * rx * (two.y * inv_d);
         float gy[NV][V], sy = 0.f;
 #pragma unroll
@@ -252,22 +394,22 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256, TPR > 256 ? 1 : 2)
                 gy[i][j] = dn * wo[i].get(j);
                 sy = fmaf(gy[i][j], in.y[i].get(j), sy);
             }
-            if (c < D) {
+            if (live && c < D) {
                 store<V>((TX *)a.dx + at + c, dx);
                 if (gated) store<V>((T *)a.dgate + at + c, dg);
             }
         }
-        const float ky = ry * ry * ry * (row_sum<TPR>(sy, 0.f, red[turn][2]).x * inv_d);
+        const float ky = ry * ry * ry * (row_sum<TPR>(sy, red[turn][1]) * inv_d);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * V;
             float d[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) d[j] = fmaf(ry, gy[i][j], -ky * in.y[i].get(j));
-            if (c < D) store<V>((T *)a.dy + at + c, d);
+            if (live && c < D) store<V>((T *)a.dy + at + c, d);
         }
     }
-    float *part = a.part + ((int64_t)blockIdx.x * RPC + side) * 2 * D;
+    float *part = a.part + ((int64_t)blockIdx.x * Rows::RPC + side) * 2 * D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + t) * V;
@@ -301,50 +443,75 @@ __global__ void __launch_bounds__(256) block_norm_weights_kernel(const float *pa
 }
 
 constexpr int kSMs = 148;
+constexpr size_t kRingBytes = 200 * 1024;   // of an SM, shared by its CTAs
 
-// Rows of partial weight gradients: as many CTAs as run at once, or as there are rows.
-int64_t grid_of(int64_t rows, int rpc, bool backward) {
+// Row groups of `rpc` rows over the SMs, `ctas` on each.
+int64_t grid_of(int64_t rows, int rpc, int ctas) {
     const int64_t all = (rows + rpc - 1) / rpc;
-    return backward ? (all < 2 * kSMs ? all : 2 * kSMs) : all;
+    return all < ctas * kSMs ? all : ctas * kSMs;
 }
 
-template <int V, int NV, int TPR, typename TX, typename T>
-cudaError_t launch_t(BlockNormArgs a, bool backward, cudaStream_t st) {
-    constexpr int RPC = TPR > 32 ? 1 : 8, threads = TPR > 32 ? TPR : 256;
-    const int64_t grid = grid_of(a.rows, RPC, backward);
-    if (!backward) {
-        block_norm_kernel<V, NV, TPR, TX, T><<<(unsigned)grid, threads, 0, st>>>(a);
-    } else {
-        if (grid > 0) {
-            block_norm_backward_kernel<V, NV, TPR, TX, T><<<(unsigned)grid, threads, 0, st>>>(a);
-            const cudaError_t e = cudaGetLastError();
+template <int V, int NV, int TPR, int NT, int CTAS, bool BACK, bool STAGED, typename TX, typename T>
+cudaError_t launch_s(const BlockNormArgs &a, size_t smem, cudaStream_t st) {
+    constexpr int RPC = NT / TPR;
+    const int64_t grid = grid_of(a.rows, RPC, CTAS);
+    const auto kernel = [] {
+        if constexpr (BACK) return block_norm_backward_kernel<V, NV, TPR, NT, CTAS, STAGED, TX, T>;
+        else return block_norm_kernel<V, NV, TPR, NT, CTAS, STAGED, TX, T>;
+    }();
+    if (grid > 0) {
+        if (STAGED) {
+            const cudaError_t e = cudaFuncSetAttribute(
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kRingBytes / CTAS));
             if (e != cudaSuccess) return e;
-            Profiler::mark(st);
         }
-        block_norm_weights_kernel<<<(2 * a.width + 31) / 32, 256, 0, st>>>(
-            a.part, (int)grid * RPC, a.width, a.dw_post, a.dw_pre);
+        kernel<<<(unsigned)grid, NT, smem, st>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        Profiler::mark(st);
     }
+    if (!BACK) return cudaSuccess;
+    block_norm_weights_kernel<<<(2 * a.width + 31) / 32, 256, 0, st>>>(a.part, (int)grid * RPC, a.width,
+                                                                       a.dw_post, a.dw_pre);
     const cudaError_t e = cudaGetLastError();
     Profiler::mark(st);
     return e;
 }
 
-// Threads per row: one vector a thread up to 512 of them; a row's values and the next one's
-// then fit the registers in either direction.
-template <int V, typename TX, typename T>
-cudaError_t launch_v(const BlockNormArgs &a, bool b, cudaStream_t st) {
-    const int vecs = (a.width + V - 1) / V;
-    if (vecs <= 32) return launch_t<V, 1, 32, TX, T>(a, b, st);
-    if (vecs <= 64) return launch_t<V, 1, 64, TX, T>(a, b, st);
-    if (vecs <= 128) return launch_t<V, 1, 128, TX, T>(a, b, st);
-    if (vecs <= 256) return launch_t<V, 1, 256, TX, T>(a, b, st);
-    if (vecs <= 512) return launch_t<V, 1, 512, TX, T>(a, b, st);
-    if (vecs <= 1024) return launch_t<V, 2, 512, TX, T>(a, b, st);
+// The ring takes as many stages as fit, two at least.
+template <int V, int NV, int TPR, int NT, int CTAS, bool BACK, typename TX, typename T>
+cudaError_t launch_t(BlockNormArgs a, cudaStream_t st) {
     if constexpr (V == 8) {
-        return launch_t<V, 4, 512, TX, T>(a, b, st);
+        const size_t stage = (size_t)(NT / TPR) * a.width *
+                             ((BACK ? 2 : 1) * sizeof(TX) + ((BACK ? 2 : 1) + (a.gate ? 1 : 0)) * sizeof(T));
+        const size_t fit = kRingBytes / CTAS / stage;
+        a.stages = (int)(fit < (size_t)kBlockNormStages ? fit : (size_t)kBlockNormStages);
+        if (a.stages >= 2)
+            return launch_s<V, NV, TPR, NT, CTAS, BACK, true, TX, T>(a, a.stages * stage, st);
+    }
+    return launch_s<V, NV, TPR, NT, CTAS, BACK, false, TX, T>(a, 0, st);
+}
+
+// CTAs of FNT / BNT threads and as many to an SM as their registers allow, so that one CTA's
+// barriers are hidden behind another's work.  Rows up to that many vectors take the next power
+// of two of threads, wider ones a CTA of 512 threads with several vectors each.
+constexpr int FNT = 512, FC = 2, BNT = 256, BC = 2;
+
+template <int V, bool BACK, typename TX, typename T>
+cudaError_t launch_v(const BlockNormArgs &a, cudaStream_t st) {
+    constexpr int NT = BACK ? BNT : FNT, CTAS = BACK ? BC : FC;
+    const int vecs = (a.width + V - 1) / V;
+    if (vecs <= 32) return launch_t<V, 1, 32, NT, CTAS, BACK, TX, T>(a, st);
+    if (vecs <= 64) return launch_t<V, 1, 64, NT, CTAS, BACK, TX, T>(a, st);
+    if (vecs <= 128) return launch_t<V, 1, 128, NT, CTAS, BACK, TX, T>(a, st);
+    if (vecs <= 256) return launch_t<V, 1, 256, NT, CTAS, BACK, TX, T>(a, st);
+    if (vecs <= 512) return launch_t<V, BACK ? 2 : 1, BACK ? 256 : 512, NT, CTAS, BACK, TX, T>(a, st);
+    if (vecs <= 1024) return launch_t<V, 2, 512, 512, 1, BACK, TX, T>(a, st);
+    if constexpr (V == 8) {
+        return launch_t<V, 4, 512, 512, 1, BACK, TX, T>(a, st);
     } else {
-        if (vecs <= 4096) return launch_t<V, 8, 512, TX, T>(a, b, st);
-        return launch_t<V, 32, 512, TX, T>(a, b, st);
+        if (vecs <= 4096) return launch_t<V, 8, 512, 512, 1, BACK, TX, T>(a, st);
+        return launch_t<V, 32, 512, 512, 1, BACK, TX, T>(a, st);
     }
 }
 
@@ -360,19 +527,29 @@ bool vectors(const BlockNormArgs &a) {
 }  // namespace
 
 size_t block_norm_parts(int64_t rows, int width) {
-    // rows side by side only where a row has at most 32 vectors; an upper bound for both
-    const int rpc = width <= 256 ? 8 : 1;
-    const int64_t one = grid_of(rows, 1, true), many = grid_of(rows, rpc, true) * rpc;
-    return (size_t)(one > many ? one : many);
+    // rows side by side in a CTA, for one and for eight elements a vector: the larger number
+    size_t most = 0;
+    for (int v : {1, 8}) {
+        const int vecs = (width + v - 1) / v;
+        int tpr = 32;
+        while (tpr < BNT && tpr < vecs) tpr *= 2;
+        const size_t parts = (size_t)grid_of(rows, BNT / tpr, BC) * (BNT / tpr);
+        if (parts > most) most = parts;
+    }
+    return most;
 }
 
 cudaError_t launch_block_norm(const BlockNormArgs &a, bool x_bf16, bool bf16, bool backward,
                               cudaStream_t st) {
     using bf = __nv_bfloat16;
-    const bool v = vectors(a);
-    if (x_bf16) return v ? launch_v<8, bf, bf>(a, backward, st) : launch_v<1, bf, bf>(a, backward, st);
-    if (bf16) return v ? launch_v<8, float, bf>(a, backward, st) : launch_v<1, float, bf>(a, backward, st);
-    return v ? launch_v<8, float, float>(a, backward, st) : launch_v<1, float, float>(a, backward, st);
+    auto types = [&](auto back) {
+        constexpr bool B = decltype(back)::value;
+        const bool v = vectors(a);
+        if (x_bf16) return v ? launch_v<8, B, bf, bf>(a, st) : launch_v<1, B, bf, bf>(a, st);
+        if (bf16) return v ? launch_v<8, B, float, bf>(a, st) : launch_v<1, B, float, bf>(a, st);
+        return v ? launch_v<8, B, float, float>(a, st) : launch_v<1, B, float, float>(a, st);
+    };
+    return backward ? types(std::true_type{}) : types(std::false_type{});
 }
 
 }  // namespace kda

@@ -15,7 +15,11 @@ struct BlockNormArgs {
     void *dx, *dy, *dgate;
     float *dw_post, *dw_pre;
     float *part;                                 // [block_norm_parts][2][width]
+    uint32_t *err;
+    uint32_t epoch;
+    int stages = 0;                              // of the ring (set by the launcher)
 };
+constexpr int kBlockNormStages = 8;
 constexpr int kBlockNormMaxWidth = 16384;
 size_t block_norm_parts(int64_t rows, int width);
 cudaError_t launch_block_norm(const BlockNormArgs &a, bool x_bf16, bool bf16, bool backward,

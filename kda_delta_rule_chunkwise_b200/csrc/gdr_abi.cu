@@ -36,7 +36,7 @@ kda_status check_norm(int64_t rows, int width, float scale, float eps, kda_dtype
     for (kda_dtype t : {x_dtype, dtype})
         if (t != KDA_F32 && t != KDA_BF16) return KDA_ERR_INVALID_ARG;
     if (x_dtype == KDA_BF16 && dtype == KDA_F32) return KDA_ERR_UNSUPPORTED;
-    if (width > kda::kBlockNormMaxWidth || rows > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (width > kda::kBlockNormMaxWidth || rows > INT32_MAX - 4096) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -139,7 +139,11 @@ kda_status kda_block_norm(const void *x, const void *y, const void *gate, const 
     if (!x || !y || !w_post || !w_pre || !x_new || !h) return KDA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     kda::Profiler::begin(st);
+    uint32_t *err = kda::device_error_word();
+    if (!err) return KDA_ERR_CUDA;
     kda::BlockNormArgs a{x, y, gate, w_post, w_pre, rows, width, scale, eps, x_new, h};
+    a.err = err;
+    a.epoch = kda::next_launch_epoch();
     return from_cuda(kda::launch_block_norm(a, x_dtype == KDA_BF16, dtype == KDA_BF16, false, st));
 }
 
@@ -165,9 +169,11 @@ kda_status kda_block_norm_backward(const void *x, const void *y, const void *gat
         return KDA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     kda::Profiler::begin(st);
+    uint32_t *err = kda::device_error_word();
+    if (!err) return KDA_ERR_CUDA;
     kda::BlockNormArgs a{x, y, gate, w_post, w_pre, rows, width, scale, eps, nullptr, nullptr,
                          dx_new, dh, dx, dy, dgate, dw_post, dw_pre,
-                         static_cast<float *>(workspace)};
+                         static_cast<float *>(workspace), err, kda::next_launch_epoch()};
     return from_cuda(kda::launch_block_norm(a, x_dtype == KDA_BF16, dtype == KDA_BF16, true, st));
 }
 
