@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_kernel(BlockNormArgs a) {
     const int t = threadIdx.x % TPR, side = threadIdx.x / TPR;
     const int D = a.width;
     const bool gated = a.gate != nullptr;
+    const float inv_d = 1.f / D;
     const auto copier = Rows::copier(a);
     const int first = blockIdx.x * Rows::RPC, step = gridDim.x * Rows::RPC;   // rows of a group
     const uint32_t bytes = STAGED ? Rows::stage_bytes(a) : 0u, ring_at = smem_u32(ring);
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_kernel(BlockNormArgs a) {
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) ss = fmaf(in.y[i].get(j), in.y[i].get(j), ss);
-        const float ry = rsqrtf(row_sum<TPR>(ss, red[turn][0]) / D + a.eps) * a.scale;
+        const float ry = rsqrtf(row_sum<TPR>(ss, red[turn][0]) * inv_d + a.eps) * a.scale;
         if (STAGED) {
             if (base + (int64_t)a.stages * step < a.rows)
                 Rows::issue(a, copier, (int)base + a.stages * step, ring_at + stage * bytes, bars + stage);
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_kernel(BlockNormArgs a) {
             }
             if (row < a.rows && c < D) store<V>((TX *)a.x_new + at + c, xn[i]);
         }
-        const float rx = rsqrtf(row_sum<TPR>(ss, red[turn][1]) / D + a.eps);
+        const float rx = rsqrtf(row_sum<TPR>(ss, red[turn][1]) * inv_d + a.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * V;
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_backward_kernel(BlockNorm
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) ss = fmaf(in.y[i].get(j), in.y[i].get(j), ss);
-        const float ry = rsqrtf(row_sum<TPR>(ss, red[turn][0]) / D + a.eps);
+        const float ry = rsqrtf(row_sum<TPR>(ss, red[turn][0]) * inv_d + a.eps);
         if (STAGED) {
             if (base + (int64_t)a.stages * step < a.rows)
                 Rows::issue(a, copier, (int)base + a.stages * step, ring_at + stage * bytes, bars + stage);
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_backward_kernel(BlockNorm
                 sg = fmaf(in.dh[i].get(j) * wi[i].get(j), xn[i][j], sg);
             }
         const float2 two = row_sum2<TPR>(sx, sg, red2[turn]);
-        const float rx = rsqrtf(two.x / D + a.eps), kx = rx * rx * rx * (two.y * inv_d);
+        const float rx = rsqrtf(two.x * inv_d + a.eps), kx = rx * rx * rx * (two.y * inv_d);
         float gy[NV][V], sy = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -422,22 +423,22 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_backward_kernel(BlockNorm
     }
 }
 
-// Column sums of part[parts][2 D] in a fixed order: 32 columns and 8 groups of rows per CTA.
-__global__ void __launch_bounds__(256) block_norm_weights_kernel(const float *part, int parts,
-                                                                 int D, float *dw_post,
-                                                                 float *dw_pre) {
-    __shared__ float red[8][33];
+// Column sums of part[parts][2 D] in a fixed order: 32 columns and 32 groups of rows per CTA.
+__global__ void __launch_bounds__(1024) block_norm_weights_kernel(const float *part, int parts,
+                                                                  int D, float *dw_post,
+                                                                  float *dw_pre) {
+    __shared__ float red[32][33];
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), group = threadIdx.x >> 5;
     float s = 0.f;
     if (col < 2 * D)
-#pragma unroll 8
-        for (int i = group; i < parts; i += 8) s += part[(int64_t)i * 2 * D + col];
+#pragma unroll 4
+        for (int i = group; i < parts; i += 32) s += part[(int64_t)i * 2 * D + col];
     red[group][threadIdx.x & 31] = s;
     __syncthreads();
     if (group == 0 && col < 2 * D) {
         s = 0.f;
 #pragma unroll
-        for (int g = 0; g < 8; ++g) s += red[g][threadIdx.x];
+        for (int g = 0; g < 32; ++g) s += red[g][threadIdx.x];
         (col < D ? dw_post[col] : dw_pre[col - D]) = s;
     }
 }
@@ -471,7 +472,7 @@ cudaError_t launch_s(const BlockNormArgs &a, size_t smem, cudaStream_t st) {
         Profiler::mark(st);
     }
     if (!BACK) return cudaSuccess;
-    block_norm_weights_kernel<<<(2 * a.width + 31) / 32, 256, 0, st>>>(a.part, (int)grid * RPC, a.width,
+    block_norm_weights_kernel<<<(2 * a.width + 31) / 32, 1024, 0, st>>>(a.part, (int)grid * RPC, a.width,
                                                                        a.dw_post, a.dw_pre);
     const cudaError_t e = cudaGetLastError();
     Profiler::mark(st);
@@ -495,7 +496,7 @@ cudaError_t launch_t(BlockNormArgs a, cudaStream_t st) {
 // CTAs of FNT / BNT threads and as many to an SM as their registers allow, so that one CTA's
 // barriers are hidden behind another's work.  Rows up to that many vectors take the next power
 // of two of threads, wider ones a CTA of 512 threads with several vectors each.
-constexpr int FNT = 512, FC = 2, BNT = 256, BC = 2;
+constexpr int FNT = 512, FC = 2, BNT = 512, BC = 1;
 
 template <int V, bool BACK, typename TX, typename T>
 cudaError_t launch_v(const BlockNormArgs &a, cudaStream_t st) {
@@ -505,7 +506,7 @@ cudaError_t launch_v(const BlockNormArgs &a, cudaStream_t st) {
     if (vecs <= 64) return launch_t<V, 1, 64, NT, CTAS, BACK, TX, T>(a, st);
     if (vecs <= 128) return launch_t<V, 1, 128, NT, CTAS, BACK, TX, T>(a, st);
     if (vecs <= 256) return launch_t<V, 1, 256, NT, CTAS, BACK, TX, T>(a, st);
-    if (vecs <= 512) return launch_t<V, BACK ? 2 : 1, BACK ? 256 : 512, NT, CTAS, BACK, TX, T>(a, st);
+    if (vecs <= 512) return launch_t<V, 1, 512, NT, CTAS, BACK, TX, T>(a, st);
     if (vecs <= 1024) return launch_t<V, 2, 512, 512, 1, BACK, TX, T>(a, st);
     if constexpr (V == 8) {
         return launch_t<V, 4, 512, 512, 1, BACK, TX, T>(a, st);
