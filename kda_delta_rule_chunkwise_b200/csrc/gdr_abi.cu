@@ -61,7 +61,7 @@ kda_status kda_gdr_chunk_prefill(const void *q, const void *k, const void *v, co
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     kda::Profiler::begin(st);
     if (dtype == KDA_BF16) {
-        const kda::GdrArgs a{q, k, v, g, beta, state_in, cu_seqlens, T, N, Hk, H, dk, dv,
+        const kda::GdrArgs a{q, k, v, g, beta, state_in, cu_seqlens, T, B * T, N, Hk, H, dk, dv,
                              o, state_out, err, kda::next_launch_epoch()};
         return from_cuda(kda::launch_gdr_prefill(a, st));
     }
@@ -123,7 +123,7 @@ kda_status kda_gdr_backward(const void *q, const void *k, const void *v, const v
     if (!err) return KDA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     kda::Profiler::begin(st);
-    const kda::GdrArgs a{q, k, v, g, beta, state_in, cu_seqlens, T, N, Hk, H, dk, dv,
+    const kda::GdrArgs a{q, k, v, g, beta, state_in, cu_seqlens, T, B * T, N, Hk, H, dk, dv,
                          nullptr, nullptr, err, kda::next_launch_epoch()};
     const kda::GdrGrads gr{dout, dstate_out, dq, dk_out, dv_out, dg, dbeta, dstate_in};
     return from_cuda(kda::launch_gdr_backward(a, gr, rows, dtype == KDA_BF16, workspace, st));

@@ -39,7 +39,7 @@ struct AdjointArgs {
     const __nv_bfloat16 *q, *k, *dout, *g, *beta;
     const float *dstate_out;
     const int32_t *cu;
-    int64_t T;
+    int64_t T, rows;
     int Hk, H, dv;
     __nv_bfloat16 *dv_out;
     float *dstate_in;
@@ -48,32 +48,15 @@ struct AdjointArgs {
     uint32_t epoch;
 };
 
-template <int DK, int NCW, int KS>
-struct AdjointSmem {
-    using L = Stage<DK, NCW * 16, true>;
-    static constexpr int OP = 48;
-    static constexpr int XF = 16;
-    static constexpr int ST = NCW == 8 ? 4 : 6;
-    static constexpr int SCRATCH = ST * L::BYTES;
-    static constexpr int OUT = SCRATCH + ST * kScratch * 4;
-    static constexpr int SWAP = OUT + NCW * kChunk * OP;
-    static constexpr int BARS = SWAP + (KS == 2 ? NCW * 2 * 2 * XF * 32 * 4 : 0);
-    static constexpr int BYTES = BARS + (3 * ST + 2 * NCW) * 8 + 16;
-};
-
-// Warps, stages and the two halves of KS = 2 as in gdr_chain_kernel; chunks from last to first.
-template <int DK, int NCW, int KS>
-__global__ void __launch_bounds__((NCW * KS + AdjointSmem<DK, NCW, KS>::ST) * 32, 1)
-    gdr_adjoint_kernel(AdjointArgs a) {
-    constexpr int W = NCW * 16, NC = DK / 8 / KS, NK = DK / 16 / KS;
-    using L = Stage<DK, W, true>;
-    using M = AdjointSmem<DK, NCW, KS>;
-    constexpr int kStages = M::ST;
-    extern __shared__ __align__(128) unsigned char smem[];
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + M::BARS);
-    uint64_t *empty = full + kStages, *landed = empty + kStages;
-    uint64_t *swapped = landed + kStages;
-    volatile uint32_t *abort = reinterpret_cast<volatile uint32_t *>(swapped + 2 * NCW);
+// Warps, stages, clusters and the two halves of KS = 2 as in gdr_chain_kernel; chunks from last to
+// first.
+template <int DK, int NCW, int KS, int CL>
+__global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, true, true, 16>::WARPS * 32), 1)
+    gdr_adjoint_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AdjointArgs a) {
+    using M = Pipe<DK, NCW, KS, CL, true, true, 16>;
+    using L = typename M::L;
+    constexpr int W = M::W, NC = DK / 8 / KS, NK = DK / 16 / KS, XF = 16;
+    extern __shared__ __align__(1024) unsigned char smem[];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slices = a.dv / W;
@@ -81,35 +64,13 @@ __global__ void __launch_bounds__((NCW * KS + AdjointSmem<DK, NCW, KS>::ST) * 32
     const int h = unit % a.H, n = unit / a.H, hk = h / (a.H / a.Hk);
     const Span span = sequence_span(a.cu, n, a.T);
     const int chunks = (span.len + kChunk - 1) / kChunk;
+    const M pipe(smem, a.err, a.epoch, CL == 1 ? 0 : slice);
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, NCW * KS);
-            mbar_init(landed + i, 1);
-        }
-        for (int i = 0; i < 2 * NCW; ++i) mbar_init(swapped + i, 1);
-        mbar_fence_init();
-        *abort = 0u;
-    }
-    __syncthreads();
-
-    if (warp >= NCW * KS) {
-        const int p = warp - NCW * KS;
-        unsigned char *stage = smem + p * L::BYTES;
-        float *scratch = reinterpret_cast<float *>(smem + M::SCRATCH) + p * kScratch;
-        const ChunkSource src{a.k + (span.row * a.Hk + hk) * DK,
-                              a.q + (span.row * a.Hk + hk) * DK,
-                              a.dout + (span.row * a.H + h) * a.dv + slice * W,
-                              a.g + span.row * a.H + h, a.beta + span.row * a.H + h,
-                              (int64_t)a.Hk * DK, (int64_t)a.H * a.dv, a.H, span.len};
-        for (int i = p, it = 0; i < chunks; i += kStages, ++it) {
-            if (it > 0 && !warp_wait(empty + p, (it - 1) & 1, a.err, a.epoch, abort)) return;
-            if (!produce_chunk<DK, W, true, true>(src, (chunks - 1 - i) * kChunk, stage, scratch,
-                                                  landed + p, it & 1, a.err, a.epoch, abort))
-                return;
-            if (lane == 0) mbar_arrive(full + p);
-        }
+    if (warp >= M::CHAIN) {
+        const ChunkSource src{&maps, a.g + span.row * a.H + h, a.beta + span.row * a.H + h,
+                              (int)span.row, hk, h, slice * W, a.H, span.len};
+        pipe.template produce<true>(src, chunks);
+        pipe.finish();
         return;
     }
 
@@ -129,12 +90,34 @@ __global__ void __launch_bounds__((NCW * KS + AdjointSmem<DK, NCW, KS>::ST) * 32
     const int nrow = (lane & 7) + (lane >> 4) * 8, ncol = ((lane >> 3) & 1) * 16;
     const int trow = lane & 15, tcol = (lane >> 4) * 16;
     unsigned char *out_tile = smem + M::OUT + group * kChunk * M::OP;
+    const int64_t vstride = (int64_t)a.H * a.dv;
+    bool ok = true;
+    uint32_t pk[4][2];   // a chunk's dV in bf16; with KS = 2 written inside the next chunk
+    auto write_dv = [&](int64_t row, int valid) {   // this warp's 16 tokens with KS = 2, else all 32
+        const int t0 = KS == 2 ? part * 16 : 0;
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < 4; t += 2)
+            if (KS == 1 || t / 2 == part)
+                stsm4_t(smem_u32(out_tile) + (8 * t + nrow) * M::OP + ncol, pk[t][0], pk[t][1],
+                        pk[t + 1][0], pk[t + 1][1]);
+        __syncwarp();
+        __nv_bfloat16 *dst = a.dv_out + (row * a.H + h) * a.dv + j0;
+#pragma unroll
+        for (int i = 0; i < 2 / KS; ++i) {
+            const int tok = t0 + i * 16 + (lane >> 1);
+            const uint4 w = *reinterpret_cast<const uint4 *>(out_tile + tok * M::OP + (lane & 1) * 16);
+            if (tok < valid) *reinterpret_cast<uint4 *>(dst + tok * vstride + (lane & 1) * 8) = w;
+        }
+    };
 
     for (int it = 0; it < chunks; ++it) {
-        const int ci = chunks - 1 - it, st = it % kStages;
-        unsigned char *stage = smem + st * L::BYTES;
+        const int ci = chunks - 1 - it, st = it % M::ST;
+        unsigned char *stage = pipe.stage(st);
         const uint32_t sb = smem_u32(stage);
         const float *scal = reinterpret_cast<const float *>(stage + L::S);
+        const int64_t row = span.row + (int64_t)ci * kChunk;
+        const int valid = span.len - ci * kChunk;
         const bool block_end = (ci & 1) == 1 || it == 0;
         const int64_t blk = (first_block(span, n) + ci / 2) * a.H + h;
 
@@ -156,7 +139,8 @@ __global__ void __launch_bounds__((NCW * KS + AdjointSmem<DK, NCW, KS>::ST) * 32
         const float fz0 = row_scale(quad_max(m0), iz0), fz1 = row_scale(quad_max(m1), iz1);
         if (block_end) store_top(a.tops + (blk * (a.dv / 16) + j0 / 16) * 2, fmaxf(m0, m1), KS, part);
 
-        if (!warp_wait(full + st, (it / kStages) & 1, a.err, a.epoch, abort)) return;
+        ok = pipe.wait(pipe.full + st, (it / M::ST) & 1);
+        if (!ok) break;
 
         // Z^T K'^T, two terms of Z
         float y[4][4];
@@ -188,13 +172,15 @@ __global__ void __launch_bounds__((NCW * KS + AdjointSmem<DK, NCW, KS>::ST) * 32
         }
         if (KS == 2) {
             float4 *mine = reinterpret_cast<float4 *>(smem + M::SWAP) +
-                           (((group * 2 + (it & 1)) * 2 + part) * M::XF / 4) * 32 + lane;
-            const float4 *other = mine + (part ? -1 : 1) * (M::XF / 4) * 32;
+                           (((group * 2 + (it & 1)) * 2 + part) * XF / 4) * 32 + lane;
+            const float4 *other = mine + (part ? -1 : 1) * (XF / 4) * 32;
 #pragma unroll
             for (int t = 0; t < 4; ++t) mine[t * 32] = make_float4(y[t][0], y[t][1], y[t][2], y[t][3]);
             __syncwarp();
-            if (lane == 0) mbar_arrive(swapped + group * 2 + (part ^ 1));
-            if (!warp_wait(swapped + group * 2 + part, it & 1, a.err, a.epoch, abort)) return;
+            if (lane == 0) mbar_arrive(pipe.swapped + group * 2 + (part ^ 1));
+            if (it > 0) write_dv(row + kChunk, valid - kChunk);   // the chunk after this one
+            ok = pipe.wait(pipe.swapped + group * 2 + part, it & 1);
+            if (!ok) break;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const float4 o = other[t * 32];
@@ -207,7 +193,8 @@ __global__ void __launch_bounds__((NCW * KS + AdjointSmem<DK, NCW, KS>::ST) * 32
 #pragma unroll
         for (int t = 0; t < 4; t += 2) {
             uint32_t v[4];
-            ldsm4_t(v, sb + L::V + (8 * t + nrow) * L::VP + ncol + group * 32);
+            ldsm4_t(v, sb + L::v_at(8 * t + nrow, group * 2 + ((lane >> 3) & 1)));
+            if (valid < kChunk) clear_rows(v, 8 * t + tc, valid);   // the rows behind the sequence's end
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float2 iq = *reinterpret_cast<const float2 *>(scal + L::IQ * kChunk + 8 * (t + u) + tc);
@@ -293,8 +280,6 @@ __global__ void __launch_bounds__((NCW * KS + AdjointSmem<DK, NCW, KS>::ST) * 32
                 e[t][3] = (e[t][3] + el[t][3]) * iu1;
             }
         }
-        const int64_t row = span.row + (int64_t)ci * kChunk;
-        const int valid = span.len - ci * kChunk;
         {
             float *dst = a.e_out + (row * a.H + h) * a.dv + j0 + jr;
 #pragma unroll
@@ -303,11 +288,10 @@ __global__ void __launch_bounds__((NCW * KS + AdjointSmem<DK, NCW, KS>::ST) * 32
                 for (int x = 0; x < 4; ++x) {
                     const int tok = 8 * t + tc + (x & 1);
                     if (tok < valid && (KS == 1 || t / 2 == part))
-                        dst[(int64_t)tok * a.H * a.dv + (x >> 1) * 8] = e[t][x];
+                        dst[tok * vstride + (x >> 1) * 8] = e[t][x];
                 }
         }
         // dV = dR = beta E; then Gamma dO and -Gamma dR in the scaled units of Q' and K'
-        uint32_t pk[4][2];
         m0 = m1 = 0.f;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -373,28 +357,10 @@ __global__ void __launch_bounds__((NCW * KS + AdjointSmem<DK, NCW, KS>::ST) * 32
                 }
             }
         }
-        {   // dV, this warp's 16 tokens with KS = 2, else all 32
-            const int t0 = KS == 2 ? part * 16 : 0;
-            __syncwarp();
-#pragma unroll
-            for (int t = 0; t < 4; t += 2)
-                if (KS == 1 || t / 2 == part)
-                    stsm4_t(smem_u32(out_tile) + (8 * t + nrow) * M::OP + ncol, pk[t][0], pk[t][1],
-                            pk[t + 1][0], pk[t + 1][1]);
-            __syncwarp();
-            __nv_bfloat16 *dst = a.dv_out + (row * a.H + h) * a.dv + j0;
-#pragma unroll
-            for (int i = 0; i < 2 / KS; ++i) {
-                const int tok = t0 + i * 16 + (lane >> 1);
-                const uint4 w = *reinterpret_cast<const uint4 *>(out_tile + tok * M::OP + (lane & 1) * 16);
-                if (tok < valid)
-                    *reinterpret_cast<uint4 *>(dst + (int64_t)tok * a.H * a.dv + (lane & 1) * 8) = w;
-            }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + st);
+        if (KS == 1 || it + 1 == chunks) write_dv(row, valid);
+        pipe.release(st);
     }
-    if (a.dstate_in) {
+    if (ok && a.dstate_in) {
         float *out = a.dstate_in + state_off;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
@@ -402,6 +368,7 @@ __global__ void __launch_bounds__((NCW * KS + AdjointSmem<DK, NCW, KS>::ST) * 32
             for (int x = 0; x < 4; ++x)
                 out[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] = z[i][x];
     }
+    pipe.finish();
 }
 
 // ---------------------------------------------------------------- gradients of a block
@@ -827,27 +794,23 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
 }
 
 // ---------------------------------------------------------------- launches
-template <int DK, int NCW, int KS>
+template <int DK, int NCW, int KS, int CL>
 static cudaError_t launch_adjoint_t(const AdjointArgs &a, int64_t units, cudaStream_t st) {
-    constexpr int bytes = AdjointSmem<DK, NCW, KS>::BYTES;
-    static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
-    cudaError_t e = cudaFuncSetAttribute(gdr_adjoint_kernel<DK, NCW, KS>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    gdr_adjoint_kernel<DK, NCW, KS>
-        <<<(unsigned)(units * (a.dv / (16 * NCW))), (NCW * KS + AdjointSmem<DK, NCW, KS>::ST) * 32,
-           bytes, st>>>(a);
-    e = cudaGetLastError();
-    Profiler::mark(st);
-    return e;
+    using M = Pipe<DK, NCW, KS, CL, true, true, 16>;
+    return launch_pipe(gdr_adjoint_kernel<DK, NCW, KS, CL>, a, a.k, a.q, a.dout, a.rows, DK, M::W,
+                       units * CL, M::WARPS * 32, M::BYTES, CL, st);
 }
 
 // The split of the columns by the number of units, as for the forward chain.
 template <int DK>
 static cudaError_t launch_adjoint_d(const AdjointArgs &a, int64_t units, cudaStream_t st) {
-    if (units * (a.dv / 32) <= 148) return launch_adjoint_t<DK, 2, 2>(a, units, st);
-    if (units * (a.dv / 64) <= 148 || a.dv == 64) return launch_adjoint_t<DK, 4, 1>(a, units, st);
-    return launch_adjoint_t<DK, 8, 1>(a, units, st);
+    if (a.dv == 128) {
+        if (units * 4 <= 128) return launch_adjoint_t<DK, 2, 2, 4>(a, units, st);
+        if (units * 2 <= 148) return launch_adjoint_t<DK, 4, 1, 2>(a, units, st);
+        return launch_adjoint_t<DK, 8, 1, 1>(a, units, st);
+    }
+    if (units * 2 <= 148) return launch_adjoint_t<DK, 2, 2, 2>(a, units, st);
+    return launch_adjoint_t<DK, 4, 1, 1>(a, units, st);
 }
 
 template <int DK, int DV>
@@ -902,7 +865,7 @@ cudaError_t launch_gdr_backward(const GdrArgs &p, const GdrGrads &g, int64_t row
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)p.N * p.H;
     AdjointArgs a{(const bf *)p.q, (const bf *)p.k, (const bf *)g.dout, (const bf *)p.g, (const bf *)p.beta,
-                  g.dstate_out, p.cu_seqlens, p.T, p.Hk, p.H, p.dv, (bf *)g.dv, g.dstate_in, s.e, s.z_blocks,
+                  g.dstate_out, p.cu_seqlens, p.T, rows, p.Hk, p.H, p.dv, (bf *)g.dv, g.dstate_in, s.e, s.z_blocks,
                   s.z_tops, p.err, p.epoch};
     e = p.dk == 64 ? launch_adjoint_d<64>(a, units, st) : launch_adjoint_d<128>(a, units, st);
     if (e != cudaSuccess) return e;

@@ -35,7 +35,7 @@ struct ChainArgs {
     const __nv_bfloat16 *q, *k, *v, *g, *beta;
     const float *state_in;
     const int32_t *cu;
-    int64_t T;
+    int64_t T, rows;
     int Hk, H, dv;
     __nv_bfloat16 *o;       // prefill
     float *state_out;       // prefill
@@ -47,38 +47,76 @@ struct ChainArgs {
     uint32_t epoch;
 };
 
-template <int DK, int NCW, int KS>
-struct ChainSmem {
-    using L = Stage<DK, NCW * 16, false>;
-    static constexpr int OP = 48;   // row pitch of a warp's output tile (tokens x 16 columns)
-    static constexpr int XF = 24;   // floats a lane hands to the other half's warp
-    // chunks in flight, each with a producer warp of its own: a chunk takes a producer about
-    // four times as long as the chain
-    static constexpr int ST = NCW == 8 ? 4 : 6;
-    static constexpr int STAGES = 0;
-    static constexpr int SCRATCH = STAGES + ST * L::BYTES;
-    static constexpr int OUT = SCRATCH + ST * kScratch * 4;
-    static constexpr int SWAP = OUT + NCW * kChunk * OP;
-    static constexpr int BARS = SWAP + (KS == 2 ? NCW * 2 * 2 * XF * 32 * 4 : 0);
-    static constexpr int BYTES = BARS + (3 * ST + 2 * NCW) * 8 + 16;
+// What a chain warp needs to finish a chunk's outputs, kept in registers so that with KS = 2
+// they are finished inside the next chunk, while the two halves' warps wait for each other.
+template <int KS>
+struct ChunkOut {
+    static constexpr int NTILE = 4 / KS, T0 = KS == 2 ? 16 : 32;   // token tiles; tokens of a warp
+    uint32_t u[2][4], p[KS == 2 ? 2 : 3][4];
+    float oq[NTILE][4], i0, i1;
+    float2 cq[NTILE], iq[NTILE];
+
+    // O = Gamma Q S + P U, both in the scaled units of Q'; rounded and written through `tile`.
+    __device__ __forceinline__ void write(unsigned char *tile, int pitch, __nv_bfloat16 *dst,
+                                          int64_t stride, int part, int valid) const {
+        const int lane = threadIdx.x & 31;
+        const int nrow = (lane & 7) + (lane >> 4) * 8, ncol = ((lane >> 3) & 1) * 16;
+        float ou[NTILE][4];
+#pragma unroll
+        for (int t = 0; t < NTILE; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) ou[t][x] = 0.f;
+        // P is zero above the diagonal
+        if (KS == 2) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {   // part 0 has zeros for its second step
+                mma16816(ou[0], u[ks], p[ks][0], p[ks][1]);
+                mma16816(ou[1], u[ks], p[ks][2], p[ks][3]);
+            }
+        } else {
+            mma16816(ou[0], u[0], p[0][0], p[0][1]);
+            mma16816(ou[1], u[0], p[0][2], p[0][3]);
+            mma16816(ou[NTILE - 2], u[0], p[1][0], p[1][1]);
+            mma16816(ou[NTILE - 1], u[0], p[1][2], p[1][3]);
+            mma16816(ou[NTILE - 2], u[1], p[KS == 2 ? 1 : 2][0], p[KS == 2 ? 1 : 2][1]);
+            mma16816(ou[NTILE - 1], u[1], p[KS == 2 ? 1 : 2][2], p[KS == 2 ? 1 : 2][3]);
+        }
+        uint32_t pk[NTILE][2];
+#pragma unroll
+        for (int t = 0; t < NTILE; ++t) {
+            const __nv_bfloat162 w0 = __floats2bfloat162_rn(cq[t].x * oq[t][0] + iq[t].x * (i0 * ou[t][0]),
+                                                            cq[t].y * oq[t][1] + iq[t].y * (i0 * ou[t][1]));
+            const __nv_bfloat162 w1 = __floats2bfloat162_rn(cq[t].x * oq[t][2] + iq[t].x * (i1 * ou[t][2]),
+                                                            cq[t].y * oq[t][3] + iq[t].y * (i1 * ou[t][3]));
+            pk[t][0] = reinterpret_cast<const uint32_t &>(w0);
+            pk[t][1] = reinterpret_cast<const uint32_t &>(w1);
+        }
+        const int t0 = part * 16;   // 0 with KS = 1
+        __syncwarp();               // the rows written before have been read out of the tile
+#pragma unroll
+        for (int t = 0; t < NTILE; t += 2)
+            stsm4_t(smem_u32(tile) + (t0 + 8 * t + nrow) * pitch + ncol, pk[t][0], pk[t][1], pk[t + 1][0],
+                    pk[t + 1][1]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2 / KS; ++i) {
+            const int tok = t0 + i * 16 + (lane >> 1);
+            const uint4 w = *reinterpret_cast<const uint4 *>(tile + tok * pitch + (lane & 1) * 16);
+            if (tok < valid) *reinterpret_cast<uint4 *>(dst + tok * stride + (lane & 1) * 8) = w;
+        }
+    }
 };
 
-// NCW groups of 16 columns per CTA; KS warps share a group, each with dk / KS of its
-// channels.  With KS = 2 the two warps add their partial K S (and Q S) through shared
-// memory, compute N twice, and update their own halves of S: half the products per warp
-// on the chain, for one exchange.
-template <int DK, int NCW, int KS, bool REC>
-__global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 1)
-    gdr_chain_kernel(ChainArgs a) {
-    constexpr int W = NCW * 16, NC = DK / 8 / KS, NK = DK / 16 / KS;
-    using L = Stage<DK, W, false>;
-    using M = ChainSmem<DK, NCW, KS>;
-    constexpr int kStages = M::ST;
-    extern __shared__ __align__(128) unsigned char smem[];
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + M::BARS);
-    uint64_t *empty = full + kStages, *landed = empty + kStages;
-    uint64_t *swapped = landed + kStages;
-    volatile uint32_t *abort = reinterpret_cast<volatile uint32_t *>(swapped + 2 * NCW);
+// With KS = 2 the two warps of a column group add their partial K S (and Q S) through shared
+// memory, compute N twice, and update their own halves of S: half the products per warp on the
+// chain, for one exchange.
+template <int DK, int NCW, int KS, int CL, bool REC>
+__global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, false, !REC, 24>::WARPS * 32), 1)
+    gdr_chain_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ChainArgs a) {
+    using M = Pipe<DK, NCW, KS, CL, false, !REC, 24>;
+    using L = typename M::L;
+    constexpr int W = M::W, NC = DK / 8 / KS, NK = DK / 16 / KS, XF = 24;
+    extern __shared__ __align__(1024) unsigned char smem[];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slices = a.dv / W;
@@ -86,39 +124,16 @@ __global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 
     const int h = unit % a.H, n = unit / a.H, hk = h / (a.H / a.Hk);
     const Span span = sequence_span(a.cu, n, a.T);
     const int chunks = (span.len + kChunk - 1) / kChunk;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, NCW * KS);
-            mbar_init(landed + i, 1);
-        }
-        for (int i = 0; i < 2 * NCW; ++i) mbar_init(swapped + i, 1);
-        mbar_fence_init();
-        *abort = 0u;
-    }
     if (REC && h == 0 && slice == 0)
         for (int i = threadIdx.x; 2 * i < chunks; i += blockDim.x)
             a.owners[first_block(span, n) + i] = n;
-    __syncthreads();
+    const M pipe(smem, a.err, a.epoch, CL == 1 ? 0 : slice);
 
-    if (warp >= NCW * KS) {
-        // ---- producer: chunks p, p + kStages, ... into stage p
-        const int p = warp - NCW * KS;
-        unsigned char *stage = smem + M::STAGES + p * L::BYTES;
-        float *scratch = reinterpret_cast<float *>(smem + M::SCRATCH) + p * kScratch;
-        const ChunkSource src{a.k + (span.row * a.Hk + hk) * DK,
-                              a.q + (span.row * a.Hk + hk) * DK,
-                              a.v + (span.row * a.H + h) * a.dv + slice * W,
-                              a.g + span.row * a.H + h, a.beta + span.row * a.H + h,
-                              (int64_t)a.Hk * DK, (int64_t)a.H * a.dv, a.H, span.len};
-        for (int i = p, it = 0; i < chunks; i += kStages, ++it) {
-            if (it > 0 && !warp_wait(empty + p, (it - 1) & 1, a.err, a.epoch, abort)) return;
-            if (!produce_chunk<DK, W, false, !REC>(src, i * kChunk, stage, scratch, landed + p,
-                                                   it & 1, a.err, a.epoch, abort))
-                return;
-            if (lane == 0) mbar_arrive(full + p);
-        }
+    if (warp >= M::CHAIN) {
+        const ChunkSource src{&maps, a.g + span.row * a.H + h, a.beta + span.row * a.H + h,
+                              (int)span.row, hk, h, slice * W, a.H, span.len};
+        pipe.template produce<false>(src, chunks);
+        pipe.finish();
         return;
     }
 
@@ -128,48 +143,49 @@ __global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 
     const int c0 = part * (DK / KS);
     float s[NC][4];   // S^T: (column jr, channel c0 + 8i + tc), +1, (column jr + 8, ..)
     const int64_t state_off = ((int64_t)n * a.H + h) * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
+    float sm0 = 0.f, sm1 = 0.f;   // this lane's largest |S| of its two columns
     {
         const float *in = a.state_in ? a.state_in + state_off : nullptr;
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < NC; ++i) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 s[i][x] = in ? in[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] : 0.f;
+            sm0 = fmaxf(sm0, fmaxf(fabsf(s[i][0]), fabsf(s[i][1])));
+            sm1 = fmaxf(sm1, fmaxf(fabsf(s[i][2]), fabsf(s[i][3])));
+        }
     }
     // per-lane parts of the ldmatrix addresses
     const int nrow = (lane & 7) + (lane >> 4) * 8, ncol = ((lane >> 3) & 1) * 16;   // [n][k] tiles
     const int trow = lane & 15, tcol = (lane >> 4) * 16;                            // [k][n] tiles
     unsigned char *out_tile = smem + M::OUT + group * kChunk * M::OP;
+    const int64_t vstride = (int64_t)a.H * a.dv;
+    ChunkOut<KS> out;
+    bool ok = true;
 
     for (int ci = 0; ci < chunks; ++ci) {
-        const int st = ci % kStages;
-        unsigned char *stage = smem + M::STAGES + st * L::BYTES;
+        const int st = ci % M::ST;
+        unsigned char *stage = pipe.stage(st);
         const uint32_t sb = smem_u32(stage);
         const float *scal = reinterpret_cast<const float *>(stage + L::S);
+        const int64_t row = span.row + (int64_t)ci * kChunk;
+        const int valid = span.len - ci * kChunk;
 
+        // row scales of S
+        float is0, is1;
+        const float fs0 = row_scale(quad_max(sm0), is0), fs1 = row_scale(quad_max(sm1), is1);
         if (REC && (ci & 1) == 0) {
-            const int64_t blk = first_block(span, n) + ci / 2;
-            float *dst = a.blocks + (blk * a.H + h) * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
+            const int64_t blk = (first_block(span, n) + ci / 2) * a.H + h;
+            float *dst = a.blocks + blk * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
 #pragma unroll
             for (int i = 0; i < NC; ++i)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     dst[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] = s[i][x];
+            store_top(a.tops + (blk * (a.dv / 16) + j0 / 16) * 2, fmaxf(sm0, sm1), KS, part);
         }
-        // row scales of S
-        float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            m0 = fmaxf(m0, fmaxf(fabsf(s[i][0]), fabsf(s[i][1])));
-            m1 = fmaxf(m1, fmaxf(fabsf(s[i][2]), fabsf(s[i][3])));
-        }
-        float is0, is1;
-        const float fs0 = row_scale(quad_max(m0), is0), fs1 = row_scale(quad_max(m1), is1);
-        if (REC && (ci & 1) == 0)
-            store_top(a.tops + (((first_block(span, n) + ci / 2) * a.H + h) * (a.dv / 16) + j0 / 16) * 2,
-                      fmaxf(m0, m1), KS, part);
-
-        if (!warp_wait(full + st, (ci / kStages) & 1, a.err, a.epoch, abort)) return;
+        ok = pipe.wait(pipe.full + st, (ci / M::ST) & 1);
+        if (!ok) break;
 
         // Y^T = S^T K'^T (two terms of S) and S^T Q'^T (the high term)
         float y[4][4], oq[4][4];
@@ -212,21 +228,23 @@ __global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 
             // add the other half's sums; of Q S each warp keeps 16 of the tokens.  Buffers
             // alternate: the other warp has read the ones of two chunks before by now.
             float4 *mine = reinterpret_cast<float4 *>(smem + M::SWAP) +
-                           (((group * 2 + (ci & 1)) * 2 + part) * M::XF / 4) * 32 + lane;
-            const float4 *other = mine + (part ? -1 : 1) * (M::XF / 4) * 32;
+                           (((group * 2 + (ci & 1)) * 2 + part) * XF / 4) * 32 + lane;
+            const float4 *other = mine + (part ? -1 : 1) * (XF / 4) * 32;
 #pragma unroll
             for (int t = 0; t < 4; ++t) mine[t * 32] = make_float4(y[t][0], y[t][1], y[t][2], y[t][3]);
             if (!REC) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int t = 0; t < 2; ++t)
                     mine[(4 + t) * 32] = part ? make_float4(oq[t][0], oq[t][1], oq[t][2], oq[t][3])
                                               : make_float4(oq[t + 2][0], oq[t + 2][1],
                                                             oq[t + 2][2], oq[t + 2][3]);
-                }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(swapped + group * 2 + (part ^ 1));
-            if (!warp_wait(swapped + group * 2 + part, ci & 1, a.err, a.epoch, abort)) return;
+            if (lane == 0) mbar_arrive(pipe.swapped + group * 2 + (part ^ 1));
+            if (!REC && ci > 0)   // the chunk before, all of whose 32 rows are valid
+                out.write(out_tile, M::OP, a.o + ((row - kChunk) * a.H + h) * a.dv + j0, vstride, part, kChunk);
+            ok = pipe.wait(pipe.swapped + group * 2 + part, ci & 1);
+            if (!ok) break;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const float4 o = other[t * 32];
@@ -243,12 +261,12 @@ __global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 
             }
         }
         // R = V - Gamma K S, this lane's tokens 8t + tc + {0, 1}
-        float r[4][4];
-        m0 = m1 = 0.f;
+        float r[4][4], m0 = 0.f, m1 = 0.f;
 #pragma unroll
         for (int t = 0; t < 4; t += 2) {
             uint32_t v[4];
-            ldsm4_t(v, sb + L::V + (8 * t + nrow) * L::VP + ncol + group * 32);
+            ldsm4_t(v, sb + L::v_at(8 * t + nrow, group * 2 + ((lane >> 3) & 1)));
+            if (valid < kChunk) clear_rows(v, 8 * t + tc, valid);   // the rows behind the sequence's end
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float2 c = *reinterpret_cast<const float2 *>(scal + L::CK * kChunk +
@@ -256,8 +274,7 @@ __global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 
                 r[t + u][0] = __uint_as_float(v[2 * u] << 16) - c.x * y[t + u][0];
                 r[t + u][1] = __uint_as_float(v[2 * u] & 0xffff0000u) - c.y * y[t + u][1];
                 r[t + u][2] = __uint_as_float(v[2 * u + 1] << 16) - c.x * y[t + u][2];
-                r[t + u][3] =
-                    __uint_as_float(v[2 * u + 1] & 0xffff0000u) - c.y * y[t + u][3];
+                r[t + u][3] = __uint_as_float(v[2 * u + 1] & 0xffff0000u) - c.y * y[t + u][3];
                 m0 = fmaxf(m0, fmaxf(fabsf(r[t + u][0]), fabsf(r[t + u][1])));
                 m1 = fmaxf(m1, fmaxf(fabsf(r[t + u][2]), fabsf(r[t + u][3])));
             }
@@ -299,8 +316,6 @@ __global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 
                 nn[t][3] = (nn[t][3] + nl[t][3]) * ir1;
             }
         }
-        const int64_t row = span.row + (int64_t)ci * kChunk;
-        const int valid = span.len - ci * kChunk;
         if (REC) {
             float *dst = a.n_out + (row * a.H + h) * a.dv + j0 + jr;
 #pragma unroll
@@ -308,7 +323,7 @@ __global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int tok = 8 * t + tc + (x & 1);
-                    if (tok < valid && (KS == 1 || t / 2 == part)) dst[(int64_t)tok * a.H * a.dv + (x >> 1) * 8] = nn[t][x];
+                    if (tok < valid && (KS == 1 || t / 2 == part)) dst[tok * vstride + (x >> 1) * 8] = nn[t][x];
                 }
         }
         // U = beta N in the scaled units of K', and with the decay to the chunk's end
@@ -343,6 +358,7 @@ __global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 
                 split_half(r[2 * ks + 1][0] * fu0, r[2 * ks + 1][1] * fu0, hi[ks][2], lo[ks][2]);
                 split_half(r[2 * ks + 1][2] * fu1, r[2 * ks + 1][3] * fu1, hi[ks][3], lo[ks][3]);
             }
+            sm0 = sm1 = 0.f;
 #pragma unroll
             for (int i = 0; i < NC; i += 4) {
                 float acc[4][4];
@@ -370,99 +386,78 @@ __global__ void __launch_bounds__((NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, 
                     s[i + t][1] = fmaf(gend, s[i + t][1], iu0 * acc[t][1]);
                     s[i + t][2] = fmaf(gend, s[i + t][2], iu1 * acc[t][2]);
                     s[i + t][3] = fmaf(gend, s[i + t][3], iu1 * acc[t][3]);
+                    sm0 = fmaxf(sm0, fmaxf(fabsf(s[i + t][0]), fabsf(s[i + t][1])));
+                    sm1 = fmaxf(sm1, fmaxf(fabsf(s[i + t][2]), fabsf(s[i + t][3])));
                 }
             }
         }
         if (!REC) {
-            // O = Gamma Q S + P U, both in the scaled units of Q'; with KS = 2 this warp's
-            // 16 tokens, else all 32
-            float iu0, iu1, ou[4 / KS][4];
-            const float fu0 = row_scale(quad_max(m2), iu0), fu1 = row_scale(quad_max(m3), iu1);
-            const int t0 = KS == 2 ? part * 16 : 0;   // first token
-#pragma unroll
-            for (int t = 0; t < 4 / KS; ++t)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) ou[t][x] = 0.f;
+            const float fu0 = row_scale(quad_max(m2), out.i0), fu1 = row_scale(quad_max(m3), out.i1);
+            const int t0 = KS == 2 ? part * 16 : 0;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                const uint32_t u[4] = {
-                    pack_half(nn[2 * ks][0] * fu0, nn[2 * ks][1] * fu0),
-                    pack_half(nn[2 * ks][2] * fu1, nn[2 * ks][3] * fu1),
-                    pack_half(nn[2 * ks + 1][0] * fu0, nn[2 * ks + 1][1] * fu0),
-                    pack_half(nn[2 * ks + 1][2] * fu1, nn[2 * ks + 1][3] * fu1)};
-#pragma unroll
-                for (int half = 0; half < 2 / KS; ++half) {
-                    if (ks * 16 > t0 + half * 16) continue;   // P is zero above the diagonal
-                    uint32_t b[4];
-                    ldsm4(b, sb + L::P + (t0 + 16 * half + nrow) * L::XP + ncol + ks * 32);
-                    mma16816(ou[2 * half], u, b[0], b[1]);
-                    mma16816(ou[2 * half + 1], u, b[2], b[3]);
-                }
+                out.u[ks][0] = pack_half(nn[2 * ks][0] * fu0, nn[2 * ks][1] * fu0);
+                out.u[ks][1] = pack_half(nn[2 * ks][2] * fu1, nn[2 * ks][3] * fu1);
+                out.u[ks][2] = pack_half(nn[2 * ks + 1][0] * fu0, nn[2 * ks + 1][1] * fu0);
+                out.u[ks][3] = pack_half(nn[2 * ks + 1][2] * fu1, nn[2 * ks + 1][3] * fu1);
             }
-            uint32_t pk[4 / KS][2];
+            const uint32_t pb = sb + L::P + nrow * L::XP + ncol;
+            if constexpr (KS == 2) {
+                ldsm4(out.p[0], pb + t0 * L::XP);
+                if (part) {
+                    ldsm4(out.p[1], pb + t0 * L::XP + 32);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) out.p[1][x] = 0u;
+                }
+            } else {
+                ldsm4(out.p[0], pb);
+                ldsm4(out.p[1], pb + 16 * L::XP);
+                ldsm4(out.p[2], pb + 16 * L::XP + 32);
+            }
 #pragma unroll
             for (int t = 0; t < 4 / KS; ++t) {
-                const float2 c = *reinterpret_cast<const float2 *>(scal + L::CQ * kChunk + t0 + 8 * t + tc);
-                const float2 iq = *reinterpret_cast<const float2 *>(scal + L::IQ * kChunk + t0 + 8 * t + tc);
-                const __nv_bfloat162 w0 = __floats2bfloat162_rn(
-                    c.x * oq[t][0] + iq.x * (iu0 * ou[t][0]), c.y * oq[t][1] + iq.y * (iu0 * ou[t][1]));
-                const __nv_bfloat162 w1 = __floats2bfloat162_rn(
-                    c.x * oq[t][2] + iq.x * (iu1 * ou[t][2]), c.y * oq[t][3] + iq.y * (iu1 * ou[t][3]));
-                pk[t][0] = reinterpret_cast<const uint32_t &>(w0);
-                pk[t][1] = reinterpret_cast<const uint32_t &>(w1);
-            }
-            __syncwarp();   // the last chunk's rows have been read out of the tile
+                out.cq[t] = *reinterpret_cast<const float2 *>(scal + L::CQ * kChunk + t0 + 8 * t + tc);
+                out.iq[t] = *reinterpret_cast<const float2 *>(scal + L::IQ * kChunk + t0 + 8 * t + tc);
 #pragma unroll
-            for (int t = 0; t < 4 / KS; t += 2)
-                stsm4_t(smem_u32(out_tile) + (t0 + 8 * t + nrow) * M::OP + ncol, pk[t][0], pk[t][1],
-                        pk[t + 1][0], pk[t + 1][1]);
-            __syncwarp();
-            __nv_bfloat16 *dst = a.o + (row * a.H + h) * a.dv + j0;
-#pragma unroll
-            for (int i = 0; i < 2 / KS; ++i) {
-                const int tok = t0 + i * 16 + (lane >> 1);
-                const uint4 w = *reinterpret_cast<const uint4 *>(out_tile + tok * M::OP + (lane & 1) * 16);
-                if (tok < valid)
-                    *reinterpret_cast<uint4 *>(dst + (int64_t)tok * a.H * a.dv + (lane & 1) * 8) = w;
+                for (int x = 0; x < 4; ++x) out.oq[t][x] = oq[t][x];
             }
+            if (KS == 1 || ci + 1 == chunks)
+                out.write(out_tile, M::OP, a.o + (row * a.H + h) * a.dv + j0, vstride, part, valid);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + st);
+        pipe.release(st);
     }
-    if (a.state_out) {
-        float *out = a.state_out + state_off;
+    if (ok && a.state_out) {
+        float *dst = a.state_out + state_off;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                out[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] = s[i][x];
+                dst[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] = s[i][x];
     }
+    pipe.finish();
 }
 
-template <int DK, int NCW, int KS, bool REC>
+template <int DK, int NCW, int KS, int CL, bool REC>
 static cudaError_t launch_chain_t(const ChainArgs &a, int64_t units, cudaStream_t st) {
-    constexpr int bytes = ChainSmem<DK, NCW, KS>::BYTES;
-    static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
-    cudaError_t e = cudaFuncSetAttribute(gdr_chain_kernel<DK, NCW, KS, REC>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    const int64_t grid = units * (a.dv / (16 * NCW));
-    gdr_chain_kernel<DK, NCW, KS, REC>
-        <<<(unsigned)grid, (NCW * KS + ChainSmem<DK, NCW, KS>::ST) * 32, bytes, st>>>(a);
-    e = cudaGetLastError();
-    Profiler::mark(st);
-    return e;
+    using M = Pipe<DK, NCW, KS, CL, false, !REC, 24>;
+    return launch_pipe(gdr_chain_kernel<DK, NCW, KS, CL, REC>, a, a.k, a.q, a.v, a.rows, DK, M::W,
+                       units * CL, M::WARPS * 32, M::BYTES, CL, st);
 }
 
 // Columns per CTA and warps per column group.  The chain's rate is set by its warps'
 // matrix instructions (8 cycles each per SM quarter), so with few (sequence, head) units
 // the work is spread over as many SMs and warps as there are; with many, one CTA takes all
-// columns, so that the producers' work is done once per chunk.
+// columns, so that the producers' work is done once per chunk without a cluster.
 template <int DK, bool REC>
 static cudaError_t launch_chain_d(const ChainArgs &a, int64_t units, cudaStream_t st) {
-    if (units * (a.dv / 32) <= 148) return launch_chain_t<DK, 2, 2, REC>(a, units, st);
-    if (units * (a.dv / 64) <= 148 || a.dv == 64) return launch_chain_t<DK, 4, 1, REC>(a, units, st);
-    return launch_chain_t<DK, 8, 1, REC>(a, units, st);
+    if (a.dv == 128) {
+        if (units * 4 <= 128) return launch_chain_t<DK, 2, 2, 4, REC>(a, units, st);
+        if (units * 2 <= 148) return launch_chain_t<DK, 4, 1, 2, REC>(a, units, st);
+        return launch_chain_t<DK, 8, 1, 1, REC>(a, units, st);
+    }
+    if (units * 2 <= 148) return launch_chain_t<DK, 2, 2, 2, REC>(a, units, st);
+    return launch_chain_t<DK, 4, 1, 1, REC>(a, units, st);
 }
 
 }  // namespace gdr
@@ -470,7 +465,7 @@ static cudaError_t launch_chain_d(const ChainArgs &a, int64_t units, cudaStream_
 cudaError_t launch_gdr_prefill(const GdrArgs &p, cudaStream_t st) {
     using bf = __nv_bfloat16;
     gdr::ChainArgs a{(const bf *)p.q, (const bf *)p.k, (const bf *)p.v, (const bf *)p.g,
-                     (const bf *)p.beta, p.state_in, p.cu_seqlens, p.T, p.Hk, p.H, p.dv,
+                     (const bf *)p.beta, p.state_in, p.cu_seqlens, p.T, p.rows, p.Hk, p.H, p.dv,
                      (bf *)p.o, p.state_out, nullptr, nullptr, nullptr, nullptr, p.err, p.epoch};
     const int64_t units = (int64_t)p.N * p.H;
     return p.dk == 64 ? gdr::launch_chain_d<64, false>(a, units, st)
@@ -480,7 +475,7 @@ cudaError_t launch_gdr_prefill(const GdrArgs &p, cudaStream_t st) {
 cudaError_t launch_gdr_recompute(const GdrArgs &p, const GdrBackwardSpace &w, cudaStream_t st) {
     using bf = __nv_bfloat16;
     gdr::ChainArgs a{(const bf *)p.q, (const bf *)p.k, (const bf *)p.v, (const bf *)p.g,
-                     (const bf *)p.beta, p.state_in, p.cu_seqlens, p.T, p.Hk, p.H, p.dv,
+                     (const bf *)p.beta, p.state_in, p.cu_seqlens, p.T, p.rows, p.Hk, p.H, p.dv,
                      nullptr, nullptr, w.n, w.s_blocks, w.s_tops, w.owners, p.err, p.epoch};
     const int64_t units = (int64_t)p.N * p.H;
     return p.dk == 64 ? gdr::launch_chain_d<64, true>(a, units, st)

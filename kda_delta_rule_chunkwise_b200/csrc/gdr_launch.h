@@ -10,6 +10,7 @@ struct GdrArgs {
     const float *state_in;
     const int32_t *cu_seqlens;   // device, N + 1 entries, or nullptr
     int64_t T;                   // rows per batch entry (packed rows when cu_seqlens)
+    int64_t rows;                // of all batch entries
     int N, Hk, H, dk, dv;
     void *o;
     float *state_out;
