@@ -409,19 +409,24 @@ KDA_API kda_status kda_chunk_prefill_host(const void *q, const void *k, const vo
 
 /*
  * Chunked prefill over whole sequences; arguments and cu_seqlens rules as for
- * kda_chunk_prefill, without a workspace.  bf16 runs on the tensor cores as one
- * launch, fp32 token by token in fp32.
+ * kda_chunk_prefill.  bf16 runs on the tensor cores (a kernel over all 32-token chunks,
+ * then the chains over them), fp32 token by token in fp32.
  *  q, k [B, T, Hk, dk];  v, o [B, T, H, dv];  g, beta [B, T, H]
  *  state_in [N, H, dk, dv] or NULL (zeros); state_out or NULL (not written).
  *  state_out may alias state_in exactly.  Rows of o that belong to no sequence
  *  are not written.
+ *  workspace  at least kda_gdr_prefill_workspace_bytes() bytes, 256-byte aligned, or NULL
+ *             when that size is 0 (fp32); its contents are read only within the call.
  */
+KDA_API size_t kda_gdr_prefill_workspace_bytes(int64_t rows, int N, int Hk, int H, int dk, int dv,
+                                               kda_dtype dtype);
 KDA_API kda_status kda_gdr_chunk_prefill(const void *q, const void *k, const void *v,
                                          const void *g, const void *beta,
                                          const float *state_in, const int32_t *cu_seqlens,
                                          int B, int64_t T, int N, int Hk, int H, int dk, int dv,
                                          kda_dtype dtype, void *o, float *state_out,
-                                         void *stream);
+                                         void *workspace,
+                                         size_t workspace_bytes, void *stream);
 
 /*
  * Decode: L tokens (one, or a few drafted ones) for each of N requests, in order,

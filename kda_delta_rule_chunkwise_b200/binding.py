@@ -40,6 +40,7 @@ EXPORTED = (
     "kda_chunk_prefill_static_scratch",
     "kda_prefill_host_workspace_bytes",
     "kda_chunk_prefill_host",
+    "kda_gdr_prefill_workspace_bytes",
     "kda_gdr_chunk_prefill",
     "kda_gdr_decode",
     "kda_gdr_backward_workspace_bytes",
@@ -112,8 +113,10 @@ def load(path: str = LIB_PATH):
                                            vp, vp, i64, vp, sz, vp]
     lib.kda_chunk_prefill_host.restype = i32
     lib.kda_gdr_chunk_prefill.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32,
-                                          i32, i32, i32, vp, vp, vp]
+                                          i32, i32, i32, vp, vp, vp, sz, vp]
     lib.kda_gdr_chunk_prefill.restype = i32
+    lib.kda_gdr_prefill_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32]
+    lib.kda_gdr_prefill_workspace_bytes.restype = sz
     lib.kda_gdr_decode.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
                                    i32, i32, i32, vp, vp]
     lib.kda_gdr_decode.restype = i32
@@ -449,6 +452,14 @@ class _Call:
             torch.cuda.set_device(self.back)
 
 
+def _space(workspace, need, device):
+    """(workspace, its bytes): the given tensor where it is large enough, else a new one."""
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if need and (have < need or workspace.device != device):
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    return workspace, have
+
+
 def _gdr_shapes(q, k, v, g, beta):
     """Sizes of a gated-delta-rule call, its five inputs checked against one another."""
     if q.dim() != 4 or v.dim() != 4:
@@ -467,7 +478,7 @@ def _gdr_shapes(q, k, v, g, beta):
 
 
 def kda_gdr_chunk_prefill(q, k, v, g, beta, state_in=None, cu_seqlens=None, *, o=None,
-                          state_out=None, want_state=True, stream=None):
+                          state_out=None, workspace=None, want_state=True, stream=None):
     """Chunked prefill of the gated delta rule (one decay per value head and token).
 
     q, k: [B, T, Hk, dk]; v: [B, T, H, dv]; g, beta: [B, T, H], all bf16 or all fp32;
@@ -487,10 +498,14 @@ def kda_gdr_chunk_prefill(q, k, v, g, beta, state_in=None, cu_seqlens=None, *, o
         o = new(v.shape, dtype=q.dtype, device=q.device)
     if state_out is None and want_state:
         state_out = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+    lib = load()
+    need = lib.kda_gdr_prefill_workspace_bytes(B * T, N, Hk, H, dk, dv, _DTYPE[q.dtype])
+    workspace, ws_bytes = _space(workspace, need, q.device)
     with _Call(q.device, stream) as raw_stream:
-        code = load().kda_gdr_chunk_prefill(
+        code = lib.kda_gdr_chunk_prefill(
             _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(state_in), _addr(cu_seqlens), B, T,
-            N, Hk, H, dk, dv, _DTYPE[q.dtype], _addr(o), _addr(state_out), raw_stream)
+            N, Hk, H, dk, dv, _DTYPE[q.dtype], _addr(o), _addr(state_out), _addr(workspace), ws_bytes,
+            raw_stream)
     _check(code, "kda_gdr_chunk_prefill")
     return o, state_out
 
@@ -538,14 +553,13 @@ def kda_gdr_backward(q, k, v, g, beta, state_in, cu_seqlens, dout, dstate_out=No
     dq, dk_, dv_, dg, db = new(q), new(k), new(v), new(g), new(beta)
     ds0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device) if want_dstate_in else None
     need = int(load().kda_gdr_backward_workspace_bytes(B * T, N, Hk, H, dk, dv, _DTYPE[q.dtype]))
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace, ws_bytes = _space(workspace, need, q.device)
     with _Call(q.device, stream) as raw_stream:
         code = load().kda_gdr_backward(
             _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(state_in), _addr(cu_seqlens), B, T,
             N, Hk, H, dk, dv, _DTYPE[q.dtype], _addr(dout), _addr(dstate_out), _addr(dq), _addr(dk_),
             _addr(dv_), _addr(dg), _addr(db), _addr(ds0), _addr(workspace),
-            workspace.numel() * workspace.element_size(), raw_stream)
+            ws_bytes, raw_stream)
     _check(code, "kda_gdr_backward")
     return dq, dk_, dv_, dg, db, ds0
 
@@ -630,9 +644,7 @@ def kda_block_norm_backward(x, y, gate, w_post, w_pre, dx_new, dh, *, scale=1.0,
     dgate = None if gate is None else torch.empty_like(gate)
     dw = torch.empty((2, D), dtype=torch.float32, device=x.device)
     need = int(load().kda_block_norm_backward_workspace_bytes(rows, D))
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _space(workspace, need, x.device)
     with _Call(x.device, stream) as raw_stream:
         code = load().kda_block_norm_backward(
             _addr(x), _addr(y), _addr(gate), _addr(w_post), _addr(w_pre), _addr(dx_new), _addr(dh), rows,

@@ -44,11 +44,19 @@ kda_status check_norm(int64_t rows, int width, float scale, float eps, kda_dtype
 
 extern "C" {
 
+size_t kda_gdr_prefill_workspace_bytes(int64_t rows, int N, int Hk, int H, int dk, int dv,
+                                       kda_dtype dtype) {
+    if (rows < 0 || N <= 0 || Hk <= 0 || H <= 0 || H % Hk != 0 || !head_dim(dk) || !head_dim(dv))
+        return 0;
+    return dtype == KDA_BF16 ? kda::gdr_image_bytes(rows, N, Hk, H, dk, false) : 0;
+}
+
 kda_status kda_gdr_chunk_prefill(const void *q, const void *k, const void *v, const void *g,
                                  const void *beta, const float *state_in,
                                  const int32_t *cu_seqlens, int B, int64_t T, int N, int Hk,
                                  int H, int dk, int dv, kda_dtype dtype, void *o,
-                                 float *state_out, void *stream) {
+                                 float *state_out, void *workspace, size_t workspace_bytes,
+                                 void *stream) {
     const kda_status s = check_sequences(cu_seqlens != nullptr, B, T, N, Hk, H, dk, dv, dtype);
     if (s != KDA_OK) return s;
     if (B * T > 0 && (!q || !k || !v || !g || !beta || !o)) return KDA_ERR_INVALID_ARG;
@@ -56,6 +64,10 @@ kda_status kda_gdr_chunk_prefill(const void *q, const void *k, const void *v, co
                           (const void *)state_out})
         if (!aligned16(p)) return KDA_ERR_INVALID_ARG;
     if (N == 0) return KDA_OK;
+    const size_t need = kda_gdr_prefill_workspace_bytes(B * T, N, Hk, H, dk, dv, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need ||
+                     (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+        return KDA_ERR_INVALID_ARG;
     uint32_t *err = kda::device_error_word();
     if (!err) return KDA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -63,7 +75,7 @@ kda_status kda_gdr_chunk_prefill(const void *q, const void *k, const void *v, co
     if (dtype == KDA_BF16) {
         const kda::GdrArgs a{q, k, v, g, beta, state_in, cu_seqlens, T, B * T, N, Hk, H, dk, dv,
                              o, state_out, err, kda::next_launch_epoch()};
-        return from_cuda(kda::launch_gdr_prefill(a, st));
+        return from_cuda(kda::launch_gdr_prefill(a, workspace, st));
     }
     const kda::GdrTokenArgs a{q, k, v, g, beta, state_in, state_out, cu_seqlens, nullptr,
                               nullptr, T, N, N, Hk, H, dk, dv, o, err};
@@ -95,7 +107,7 @@ size_t kda_gdr_backward_workspace_bytes(int64_t rows, int N, int Hk, int H, int 
                                         kda_dtype dtype) {
     if (rows < 0 || N < 0 || Hk <= 0 || H <= 0 || H % Hk != 0 || !head_dim(dk) || !head_dim(dv))
         return 0;
-    return kda::gdr_backward_workspace_bytes(rows, N, H, dk, dv, dtype == KDA_BF16);
+    return kda::gdr_backward_workspace_bytes(rows, N, Hk, H, dk, dv, dtype == KDA_BF16);
 }
 
 kda_status kda_gdr_backward(const void *q, const void *k, const void *v, const void *g,

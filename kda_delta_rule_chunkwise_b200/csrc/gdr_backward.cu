@@ -36,27 +36,22 @@ namespace kda {
 namespace gdr {
 
 struct AdjointArgs {
-    const __nv_bfloat16 *q, *k, *dout, *g, *beta;
+    ChainInput in;
     const float *dstate_out;
-    const int32_t *cu;
-    int64_t T, rows;
-    int Hk, H, dv;
     __nv_bfloat16 *dv_out;
     float *dstate_in;
     float *e_out, *blocks, *tops;
-    uint32_t *err;
-    uint32_t epoch;
 };
 
-// Warps, stages, clusters and the two halves of KS = 2 as in gdr_chain_kernel; chunks from last to
-// first.
-template <int DK, int NCW, int KS, int CL>
-__global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, true, true, 16>::WARPS * 32), 1)
-    gdr_adjoint_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AdjointArgs a) {
-    using M = Pipe<DK, NCW, KS, CL, true, true, 16>;
+// Warps, stages and the two halves of KS = 2 as in gdr_chain_kernel; chunks from last to first.
+template <int DK, int NCW, int KS>
+__global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32), 1)
+    gdr_adjoint_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_constant__ AdjointArgs args) {
+    using M = Pipe<DK, NCW, KS, true, true, 0>;
     using L = typename M::L;
     constexpr int W = M::W, NC = DK / 8 / KS, NK = DK / 16 / KS, XF = 16;
     extern __shared__ __align__(1024) unsigned char smem[];
+    const ChainInput &a = args.in;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slices = a.dv / W;
@@ -64,13 +59,10 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, true, true, 16>::WARPS 
     const int h = unit % a.H, n = unit / a.H, hk = h / (a.H / a.Hk);
     const Span span = sequence_span(a.cu, n, a.T);
     const int chunks = (span.len + kChunk - 1) / kChunk;
-    const M pipe(smem, a.err, a.epoch, CL == 1 ? 0 : slice);
+    const M pipe(smem, a.err, a.epoch);
 
     if (warp >= M::CHAIN) {
-        const ChunkSource src{&maps, a.g + span.row * a.H + h, a.beta + span.row * a.H + h,
-                              (int)span.row, hk, h, slice * W, a.H, span.len};
-        pipe.template produce<true>(src, chunks);
-        pipe.finish();
+        pipe.template load<true>(a, &vmap, span, n, h, hk, slice * W, chunks);
         return;
     }
 
@@ -80,7 +72,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, true, true, 16>::WARPS 
     float z[NC][4];   // Z^T, laid out like the forward's S^T
     const int64_t state_off = ((int64_t)n * a.H + h) * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
     {
-        const float *in = a.dstate_out ? a.dstate_out + state_off : nullptr;
+        const float *in = args.dstate_out ? args.dstate_out + state_off : nullptr;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -102,7 +94,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, true, true, 16>::WARPS 
                 stsm4_t(smem_u32(out_tile) + (8 * t + nrow) * M::OP + ncol, pk[t][0], pk[t][1],
                         pk[t + 1][0], pk[t + 1][1]);
         __syncwarp();
-        __nv_bfloat16 *dst = a.dv_out + (row * a.H + h) * a.dv + j0;
+        __nv_bfloat16 *dst = args.dv_out + (row * a.H + h) * a.dv + j0;
 #pragma unroll
         for (int i = 0; i < 2 / KS; ++i) {
             const int tok = t0 + i * 16 + (lane >> 1);
@@ -122,7 +114,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, true, true, 16>::WARPS 
         const int64_t blk = (first_block(span, n) + ci / 2) * a.H + h;
 
         if (block_end) {
-            float *dst = a.blocks + blk * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
+            float *dst = args.blocks + blk * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
 #pragma unroll
             for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -137,7 +129,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, true, true, 16>::WARPS 
         }
         float iz0, iz1;
         const float fz0 = row_scale(quad_max(m0), iz0), fz1 = row_scale(quad_max(m1), iz1);
-        if (block_end) store_top(a.tops + (blk * (a.dv / 16) + j0 / 16) * 2, fmaxf(m0, m1), KS, part);
+        if (block_end) store_top(args.tops + (blk * (a.dv / 16) + j0 / 16) * 2, fmaxf(m0, m1), KS, part);
 
         ok = pipe.wait(pipe.full + st, (it / M::ST) & 1);
         if (!ok) break;
@@ -281,7 +273,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, true, true, 16>::WARPS 
             }
         }
         {
-            float *dst = a.e_out + (row * a.H + h) * a.dv + j0 + jr;
+            float *dst = args.e_out + (row * a.H + h) * a.dv + j0 + jr;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -360,15 +352,14 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, true, true, 16>::WARPS 
         if (KS == 1 || it + 1 == chunks) write_dv(row, valid);
         pipe.release(st);
     }
-    if (ok && a.dstate_in) {
-        float *out = a.dstate_in + state_off;
+    if (ok && args.dstate_in) {
+        float *out = args.dstate_in + state_off;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 out[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] = z[i][x];
     }
-    pipe.finish();
 }
 
 // ---------------------------------------------------------------- gradients of a block
@@ -794,23 +785,21 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
 }
 
 // ---------------------------------------------------------------- launches
-template <int DK, int NCW, int KS, int CL>
-static cudaError_t launch_adjoint_t(const AdjointArgs &a, int64_t units, cudaStream_t st) {
-    using M = Pipe<DK, NCW, KS, CL, true, true, 16>;
-    return launch_pipe(gdr_adjoint_kernel<DK, NCW, KS, CL>, a, a.k, a.q, a.dout, a.rows, DK, M::W,
-                       units * CL, M::WARPS * 32, M::BYTES, CL, st);
+template <int DK, int NCW, int KS>
+static cudaError_t launch_adjoint_t(const AdjointArgs &a, const void *dout, int64_t rows, int64_t units,
+                                    cudaStream_t st) {
+    using M = Pipe<DK, NCW, KS, true, true, 0>;
+    return launch_chain_kernel(gdr_adjoint_kernel<DK, NCW, KS>, a, dout, rows, M::W, units, M::WARPS * 32, M::BYTES,
+                               st);
 }
 
 // The split of the columns by the number of units, as for the forward chain.
 template <int DK>
-static cudaError_t launch_adjoint_d(const AdjointArgs &a, int64_t units, cudaStream_t st) {
-    if (a.dv == 128) {
-        if (units * 4 <= 128) return launch_adjoint_t<DK, 2, 2, 4>(a, units, st);
-        if (units * 2 <= 148) return launch_adjoint_t<DK, 4, 1, 2>(a, units, st);
-        return launch_adjoint_t<DK, 8, 1, 1>(a, units, st);
-    }
-    if (units * 2 <= 148) return launch_adjoint_t<DK, 2, 2, 2>(a, units, st);
-    return launch_adjoint_t<DK, 4, 1, 1>(a, units, st);
+static cudaError_t launch_adjoint_d(const AdjointArgs &a, const void *dout, int64_t rows, int64_t units,
+                                    cudaStream_t st) {
+    if (units * (a.in.dv / 32) <= 148) return launch_adjoint_t<DK, 2, 2>(a, dout, rows, units, st);
+    if (units * (a.in.dv / 64) <= 148 || a.in.dv == 64) return launch_adjoint_t<DK, 4, 1>(a, dout, rows, units, st);
+    return launch_adjoint_t<DK, 8, 1>(a, dout, rows, units, st);
 }
 
 template <int DK, int DV>
@@ -831,12 +820,12 @@ static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace gdr
 
-size_t gdr_backward_workspace_bytes(int64_t rows, int N, int H, int dk, int dv, bool bf16) {
+size_t gdr_backward_workspace_bytes(int64_t rows, int N, int Hk, int H, int dk, int dv, bool bf16) {
     using namespace gdr;
     if (!bf16) return token_backward_workspace_bytes(rows, N, H, dk, dv);
     const size_t slots = (size_t)block_slots(rows, N) * H;
     return 2 * (up256((size_t)rows * H * dv * 4) + up256(slots * dk * dv * 4) + up256(slots * (dv / 8) * 4)) +
-           up256(slots / H * 4);
+           up256(slots / H * 4) + gdr_image_bytes(rows, N, Hk, H, dk, true);
 }
 
 cudaError_t launch_gdr_backward(const GdrArgs &p, const GdrGrads &g, int64_t rows, bool bf16,
@@ -861,13 +850,15 @@ cudaError_t launch_gdr_backward(const GdrArgs &p, const GdrGrads &g, int64_t row
     s.owners = reinterpret_cast<int32_t *>(take(slots / p.H * 4));
     cudaError_t e = cudaMemsetAsync(s.owners, 0xff, slots / p.H * 4, st);
     if (e != cudaSuccess) return e;
-    e = launch_gdr_recompute(p, s, st);
+    const GdrImages m = gdr_images(w, rows, p.N, p.Hk, p.H, p.dk, true);
+    e = launch_gdr_prep(p, m, st);
+    if (e != cudaSuccess) return e;
+    e = launch_gdr_recompute(p, m, s, st);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)p.N * p.H;
-    AdjointArgs a{(const bf *)p.q, (const bf *)p.k, (const bf *)g.dout, (const bf *)p.g, (const bf *)p.beta,
-                  g.dstate_out, p.cu_seqlens, p.T, rows, p.Hk, p.H, p.dv, (bf *)g.dv, g.dstate_in, s.e, s.z_blocks,
-                  s.z_tops, p.err, p.epoch};
-    e = p.dk == 64 ? launch_adjoint_d<64>(a, units, st) : launch_adjoint_d<128>(a, units, st);
+    AdjointArgs a{{m.keys, m.adjoint, p.cu_seqlens, p.T, p.Hk, p.H, p.dv, p.err, p.epoch},
+                  g.dstate_out, (bf *)g.dv, g.dstate_in, s.e, s.z_blocks, s.z_tops};
+    e = p.dk == 64 ? launch_adjoint_d<64>(a, g.dout, rows, units, st) : launch_adjoint_d<128>(a, g.dout, rows, units, st);
     if (e != cudaSuccess) return e;
     GradsArgs b{(const bf *)p.q, (const bf *)p.k, (const bf *)g.dout, (const bf *)p.g, (const bf *)p.beta,
                 s.n, s.e, s.s_blocks, s.z_blocks, s.s_tops, s.z_tops, p.cu_seqlens, s.owners, p.T, p.Hk, p.H,

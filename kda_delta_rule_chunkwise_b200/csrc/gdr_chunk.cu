@@ -17,8 +17,7 @@
 // transposed form take their left operand from the previous product's accumulators in
 // place (an m16n8 accumulator pair is an m16k16 operand), so the chain over chunks never
 // leaves the warp: no shared memory, no barrier between its products.  The right operands
-// (K, Q, X, P) are the same for all columns; four to six producer warps make them in shared
-// memory, each a chunk of its own, ahead of the chain.
+// (K, Q, X, P) are the same for all columns; gdr_prep_kernel makes them, all chunks at once.
 //
 // Precision: S, V - Gamma K S and beta N enter the products as fp16 hi + lo of the row
 // scaled by a power of two (22 bits), K and Q are exact in fp16 after a power-of-two scale
@@ -32,91 +31,95 @@ namespace kda {
 namespace gdr {
 
 struct ChainArgs {
-    const __nv_bfloat16 *q, *k, *v, *g, *beta;
+    ChainInput in;
     const float *state_in;
-    const int32_t *cu;
-    int64_t T, rows;
-    int Hk, H, dv;
     __nv_bfloat16 *o;       // prefill
     float *state_out;       // prefill
     float *n_out;           // recomputation: N [rows, H, dv]
     float *blocks;          // recomputation: state before each 64-token block [.., H, dk, dv]
     float *tops;            // recomputation: largest |state| of each block's parts [.., H, dv/16, 2]
     int32_t *owners;        // recomputation: the sequence of each block
-    uint32_t *err;
-    uint32_t epoch;
 };
 
-// What a chain warp needs to finish a chunk's outputs, kept in registers so that with KS = 2
-// they are finished inside the next chunk, while the two halves' warps wait for each other.
-template <int KS>
+// What finishes a chunk's outputs of a column group: O = Gamma Q S + P U, both in the scaled units
+// of Q', rounded and written through `tile`.
 struct ChunkOut {
-    static constexpr int NTILE = 4 / KS, T0 = KS == 2 ? 16 : 32;   // token tiles; tokens of a warp
-    uint32_t u[2][4], p[KS == 2 ? 2 : 3][4];
-    float oq[NTILE][4], i0, i1;
-    float2 cq[NTILE], iq[NTILE];
+    uint32_t u[2][4], p[3][4];   // U^T (16 columns x 32 tokens); P's blocks (0,0) (1,0) (1,1)
+    float oq[4][4], i0, i1;
+    float2 cq[4], iq[4];
 
-    // O = Gamma Q S + P U, both in the scaled units of Q'; rounded and written through `tile`.
+    // P and the row scalars of the chunk in a stage
+    template <typename L>
+    __device__ __forceinline__ void read_stage(uint32_t sb, const float *scal) {
+        const int lane = threadIdx.x & 31, tc = 2 * (lane & 3);
+        const uint32_t pb = sb + L::P + ((lane & 7) + (lane >> 4) * 8) * L::XP + ((lane >> 3) & 1) * 16;
+        ldsm4(p[0], pb);
+        ldsm4(p[1], pb + 16 * L::XP);
+        ldsm4(p[2], pb + 16 * L::XP + 32);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            cq[t] = *reinterpret_cast<const float2 *>(scal + L::CQ * kChunk + 8 * t + tc);
+            iq[t] = *reinterpret_cast<const float2 *>(scal + L::IQ * kChunk + 8 * t + tc);
+        }
+    }
     __device__ __forceinline__ void write(unsigned char *tile, int pitch, __nv_bfloat16 *dst,
-                                          int64_t stride, int part, int valid) const {
+                                          int64_t stride, int valid) const {
         const int lane = threadIdx.x & 31;
         const int nrow = (lane & 7) + (lane >> 4) * 8, ncol = ((lane >> 3) & 1) * 16;
-        float ou[NTILE][4];
+        float ou[4][4];
 #pragma unroll
-        for (int t = 0; t < NTILE; ++t)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int x = 0; x < 4; ++x) ou[t][x] = 0.f;
-        // P is zero above the diagonal
-        if (KS == 2) {
+        mma16816(ou[0], u[0], p[0][0], p[0][1]);
+        mma16816(ou[1], u[0], p[0][2], p[0][3]);
+        mma16816(ou[2], u[0], p[1][0], p[1][1]);
+        mma16816(ou[3], u[0], p[1][2], p[1][3]);
+        mma16816(ou[2], u[1], p[2][0], p[2][1]);
+        mma16816(ou[3], u[1], p[2][2], p[2][3]);
+        __syncwarp();   // the rows written before have been read out of the tile
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {   // part 0 has zeros for its second step
-                mma16816(ou[0], u[ks], p[ks][0], p[ks][1]);
-                mma16816(ou[1], u[ks], p[ks][2], p[ks][3]);
+        for (int t = 0; t < 4; t += 2) {
+            uint32_t pk[2][2];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const int i = t + v;
+                const __nv_bfloat162 w0 = __floats2bfloat162_rn(cq[i].x * oq[i][0] + iq[i].x * (i0 * ou[i][0]),
+                                                                cq[i].y * oq[i][1] + iq[i].y * (i0 * ou[i][1]));
+                const __nv_bfloat162 w1 = __floats2bfloat162_rn(cq[i].x * oq[i][2] + iq[i].x * (i1 * ou[i][2]),
+                                                                cq[i].y * oq[i][3] + iq[i].y * (i1 * ou[i][3]));
+                pk[v][0] = reinterpret_cast<const uint32_t &>(w0);
+                pk[v][1] = reinterpret_cast<const uint32_t &>(w1);
             }
-        } else {
-            mma16816(ou[0], u[0], p[0][0], p[0][1]);
-            mma16816(ou[1], u[0], p[0][2], p[0][3]);
-            mma16816(ou[NTILE - 2], u[0], p[1][0], p[1][1]);
-            mma16816(ou[NTILE - 1], u[0], p[1][2], p[1][3]);
-            mma16816(ou[NTILE - 2], u[1], p[KS == 2 ? 1 : 2][0], p[KS == 2 ? 1 : 2][1]);
-            mma16816(ou[NTILE - 1], u[1], p[KS == 2 ? 1 : 2][2], p[KS == 2 ? 1 : 2][3]);
+            stsm4_t(smem_u32(tile) + (8 * t + nrow) * pitch + ncol, pk[0][0], pk[0][1], pk[1][0], pk[1][1]);
         }
-        uint32_t pk[NTILE][2];
-#pragma unroll
-        for (int t = 0; t < NTILE; ++t) {
-            const __nv_bfloat162 w0 = __floats2bfloat162_rn(cq[t].x * oq[t][0] + iq[t].x * (i0 * ou[t][0]),
-                                                            cq[t].y * oq[t][1] + iq[t].y * (i0 * ou[t][1]));
-            const __nv_bfloat162 w1 = __floats2bfloat162_rn(cq[t].x * oq[t][2] + iq[t].x * (i1 * ou[t][2]),
-                                                            cq[t].y * oq[t][3] + iq[t].y * (i1 * ou[t][3]));
-            pk[t][0] = reinterpret_cast<const uint32_t &>(w0);
-            pk[t][1] = reinterpret_cast<const uint32_t &>(w1);
-        }
-        const int t0 = part * 16;   // 0 with KS = 1
-        __syncwarp();               // the rows written before have been read out of the tile
-#pragma unroll
-        for (int t = 0; t < NTILE; t += 2)
-            stsm4_t(smem_u32(tile) + (t0 + 8 * t + nrow) * pitch + ncol, pk[t][0], pk[t][1], pk[t + 1][0],
-                    pk[t + 1][1]);
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 2 / KS; ++i) {
-            const int tok = t0 + i * 16 + (lane >> 1);
+        for (int i = 0; i < 2; ++i) {
+            const int tok = i * 16 + (lane >> 1);
             const uint4 w = *reinterpret_cast<const uint4 *>(tile + tok * pitch + (lane & 1) * 16);
             if (tok < valid) *reinterpret_cast<uint4 *>(dst + tok * stride + (lane & 1) * 8) = w;
         }
     }
 };
+// The hand-over of a chunk from a group's two chain warps to its output warp (KS = 2): per lane the
+// two partial Q S (4 float4 each), U^T as packed and its two scales.
+constexpr int kHandOq = 0, kHandU = 2 * 4 * 512, kHandScale = kHandU + 2 * 512;
+constexpr int kHandBytes = kHandScale + 256;
+template <int KS, bool REC>
+constexpr int hand_bytes() { return KS == 2 && !REC ? kHandBytes : 0; }
 
-// With KS = 2 the two warps of a column group add their partial K S (and Q S) through shared
-// memory, compute N twice, and update their own halves of S: half the products per warp on the
-// chain, for one exchange.
-template <int DK, int NCW, int KS, int CL, bool REC>
-__global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, false, !REC, 24>::WARPS * 32), 1)
-    gdr_chain_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ChainArgs a) {
-    using M = Pipe<DK, NCW, KS, CL, false, !REC, 24>;
+// With KS = 2 the two warps of a column group add their partial K S through shared memory, compute
+// N twice, and update their own halves of S: half the products per warp on the chain, for one
+// exchange; and the outputs are left to an output warp per group.
+template <int DK, int NCW, int KS, bool REC>
+__global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS, REC>()>::WARPS * 32), 1)
+    gdr_chain_kernel(const __grid_constant__ CUtensorMap vmap, const __grid_constant__ ChainArgs args) {
+    using M = Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS, REC>()>;
     using L = typename M::L;
-    constexpr int W = M::W, NC = DK / 8 / KS, NK = DK / 16 / KS, XF = 24;
+    constexpr int W = M::W, NC = DK / 8 / KS, NK = DK / 16 / KS;
     extern __shared__ __align__(1024) unsigned char smem[];
+    const ChainInput &a = args.in;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slices = a.dv / W;
@@ -126,14 +129,48 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, false, !REC, 24>::WARPS
     const int chunks = (span.len + kChunk - 1) / kChunk;
     if (REC && h == 0 && slice == 0)
         for (int i = threadIdx.x; 2 * i < chunks; i += blockDim.x)
-            a.owners[first_block(span, n) + i] = n;
-    const M pipe(smem, a.err, a.epoch, CL == 1 ? 0 : slice);
+            args.owners[first_block(span, n) + i] = n;
+    const M pipe(smem, a.err, a.epoch);
 
+    if (M::OW > 0 && warp > M::CHAIN) {
+        // ---- output warp of a column group
+        const int group = warp - M::CHAIN - 1;
+        unsigned char *tile = smem + M::OUT + group * kChunk * M::OP;
+        ChunkOut out;
+        for (int ci = 0; ci < chunks; ++ci) {
+            const int st = ci % M::ST, b = ci & 1;
+            const uint32_t turn = (ci >> 1) & 1;
+            if (!pipe.wait(pipe.full + st, (ci / M::ST) & 1)) break;
+            out.template read_stage<L>(smem_u32(pipe.stage(st)),
+                                       reinterpret_cast<const float *>(pipe.stage(st) + L::S));
+            if (!pipe.wait(pipe.handed + group * 2 + b, turn)) break;
+            const unsigned char *hand = pipe.hand(group, b);
+            const float4 *oq = reinterpret_cast<const float4 *>(hand + kHandOq) + lane;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const float4 x = oq[t * 32], y = oq[(4 + t) * 32];
+                out.oq[t][0] = x.x + y.x; out.oq[t][1] = x.y + y.y;
+                out.oq[t][2] = x.z + y.z; out.oq[t][3] = x.w + y.w;
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const uint4 w = reinterpret_cast<const uint4 *>(hand + kHandU)[ks * 32 + lane];
+                out.u[ks][0] = w.x; out.u[ks][1] = w.y; out.u[ks][2] = w.z; out.u[ks][3] = w.w;
+            }
+            const float2 sc = reinterpret_cast<const float2 *>(hand + kHandScale)[lane];
+            out.i0 = sc.x;
+            out.i1 = sc.y;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pipe.taken + group * 2 + b);
+            const int64_t row = span.row + (int64_t)ci * kChunk;
+            out.write(tile, M::OP, args.o + (row * a.H + h) * a.dv + slice * W + group * 16,
+                      (int64_t)a.H * a.dv, span.len - ci * kChunk);
+            pipe.release(st);   // P has been used
+        }
+        return;
+    }
     if (warp >= M::CHAIN) {
-        const ChunkSource src{&maps, a.g + span.row * a.H + h, a.beta + span.row * a.H + h,
-                              (int)span.row, hk, h, slice * W, a.H, span.len};
-        pipe.template produce<false>(src, chunks);
-        pipe.finish();
+        pipe.template load<false>(a, &vmap, span, n, h, hk, slice * W, chunks);
         return;
     }
 
@@ -145,7 +182,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, false, !REC, 24>::WARPS
     const int64_t state_off = ((int64_t)n * a.H + h) * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
     float sm0 = 0.f, sm1 = 0.f;   // this lane's largest |S| of its two columns
     {
-        const float *in = a.state_in ? a.state_in + state_off : nullptr;
+        const float *in = args.state_in ? args.state_in + state_off : nullptr;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
 #pragma unroll
@@ -160,7 +197,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, false, !REC, 24>::WARPS
     const int trow = lane & 15, tcol = (lane >> 4) * 16;                            // [k][n] tiles
     unsigned char *out_tile = smem + M::OUT + group * kChunk * M::OP;
     const int64_t vstride = (int64_t)a.H * a.dv;
-    ChunkOut<KS> out;
+    ChunkOut out;   // KS = 1: this warp writes the outputs itself
     bool ok = true;
 
     for (int ci = 0; ci < chunks; ++ci) {
@@ -176,13 +213,13 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, false, !REC, 24>::WARPS
         const float fs0 = row_scale(quad_max(sm0), is0), fs1 = row_scale(quad_max(sm1), is1);
         if (REC && (ci & 1) == 0) {
             const int64_t blk = (first_block(span, n) + ci / 2) * a.H + h;
-            float *dst = a.blocks + blk * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
+            float *dst = args.blocks + blk * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
 #pragma unroll
             for (int i = 0; i < NC; ++i)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     dst[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] = s[i][x];
-            store_top(a.tops + (blk * (a.dv / 16) + j0 / 16) * 2, fmaxf(sm0, sm1), KS, part);
+            store_top(args.tops + (blk * (a.dv / 16) + j0 / 16) * 2, fmaxf(sm0, sm1), KS, part);
         }
         ok = pipe.wait(pipe.full + st, (ci / M::ST) & 1);
         if (!ok) break;
@@ -224,60 +261,66 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, false, !REC, 24>::WARPS
             y[t][0] *= is0; y[t][1] *= is0; y[t][2] *= is1; y[t][3] *= is1;
             oq[t][0] *= is0; oq[t][1] *= is0; oq[t][2] *= is1; oq[t][3] *= is1;
         }
+        uint4 *hand = KS == 2 && !REC ? reinterpret_cast<uint4 *>(pipe.hand(group, ci & 1)) + lane : nullptr;
         if (KS == 2) {
-            // add the other half's sums; of Q S each warp keeps 16 of the tokens.  Buffers
-            // alternate: the other warp has read the ones of two chunks before by now.
+            // add the other half's sums.  Buffers alternate: the other warp has read the ones of
+            // two chunks before by now.
             float4 *mine = reinterpret_cast<float4 *>(smem + M::SWAP) +
-                           (((group * 2 + (ci & 1)) * 2 + part) * XF / 4) * 32 + lane;
-            const float4 *other = mine + (part ? -1 : 1) * (XF / 4) * 32;
+                           (((group * 2 + (ci & 1)) * 2 + part) * 4) * 32 + lane;
 #pragma unroll
             for (int t = 0; t < 4; ++t) mine[t * 32] = make_float4(y[t][0], y[t][1], y[t][2], y[t][3]);
-            if (!REC) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    mine[(4 + t) * 32] = part ? make_float4(oq[t][0], oq[t][1], oq[t][2], oq[t][3])
-                                              : make_float4(oq[t + 2][0], oq[t + 2][1],
-                                                            oq[t + 2][2], oq[t + 2][3]);
-            }
             __syncwarp();
             if (lane == 0) mbar_arrive(pipe.swapped + group * 2 + (part ^ 1));
-            if (!REC && ci > 0)   // the chunk before, all of whose 32 rows are valid
-                out.write(out_tile, M::OP, a.o + ((row - kChunk) * a.H + h) * a.dv + j0, vstride, part, kChunk);
+            if (!REC) {   // this half's Q S to the output warp, which has taken the one of two chunks before
+                ok = ci < 2 || pipe.wait(pipe.taken + group * 2 + (ci & 1), ((ci >> 1) - 1) & 1);
+                if (!ok) break;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    reinterpret_cast<float4 *>(hand)[(part * 4 + t) * 32] =
+                        make_float4(oq[t][0], oq[t][1], oq[t][2], oq[t][3]);
+            }
+        }
+        // what does not depend on the other half, while it is on its way
+        uint32_t v[2][4], xh[3][4], xl[3][4];   // values; blocks (0,0) (1,0) (1,1) of X
+        float2 ck[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            ldsm4_t(v[t], sb + L::v_at(16 * t + nrow, group * 2 + ((lane >> 3) & 1)));
+            if (valid < kChunk) clear_rows(v[t], 16 * t + tc, valid);   // rows behind the sequence's end
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ck[t] = *reinterpret_cast<const float2 *>(scal + L::CK * kChunk + 8 * t + tc);
+        {
+            const uint32_t at = sb + nrow * L::XP + ncol;
+            ldsm4(xh[0], at + L::XH);
+            ldsm4(xl[0], at + L::XL);
+            ldsm4(xh[1], at + L::XH + 16 * L::XP);
+            ldsm4(xl[1], at + L::XL + 16 * L::XP);
+            ldsm4(xh[2], at + L::XH + 16 * L::XP + 32);
+            ldsm4(xl[2], at + L::XL + 16 * L::XP + 32);
+        }
+        if (KS == 2) {
             ok = pipe.wait(pipe.swapped + group * 2 + part, ci & 1);
             if (!ok) break;
+            const float4 *other = reinterpret_cast<const float4 *>(smem + M::SWAP) +
+                                  (((group * 2 + (ci & 1)) * 2 + (part ^ 1)) * 4) * 32 + lane;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const float4 o = other[t * 32];
                 y[t][0] += o.x; y[t][1] += o.y; y[t][2] += o.z; y[t][3] += o.w;
             }
-            if (!REC) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const float4 o = other[(4 + t) * 32];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) oq[t][x] = part ? oq[t + 2][x] : oq[t][x];
-                    oq[t][0] += o.x; oq[t][1] += o.y; oq[t][2] += o.z; oq[t][3] += o.w;
-                }
-            }
         }
         // R = V - Gamma K S, this lane's tokens 8t + tc + {0, 1}
         float r[4][4], m0 = 0.f, m1 = 0.f;
 #pragma unroll
-        for (int t = 0; t < 4; t += 2) {
-            uint32_t v[4];
-            ldsm4_t(v, sb + L::v_at(8 * t + nrow, group * 2 + ((lane >> 3) & 1)));
-            if (valid < kChunk) clear_rows(v, 8 * t + tc, valid);   // the rows behind the sequence's end
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float2 c = *reinterpret_cast<const float2 *>(scal + L::CK * kChunk +
-                                                                   8 * (t + u) + tc);
-                r[t + u][0] = __uint_as_float(v[2 * u] << 16) - c.x * y[t + u][0];
-                r[t + u][1] = __uint_as_float(v[2 * u] & 0xffff0000u) - c.y * y[t + u][1];
-                r[t + u][2] = __uint_as_float(v[2 * u + 1] << 16) - c.x * y[t + u][2];
-                r[t + u][3] = __uint_as_float(v[2 * u + 1] & 0xffff0000u) - c.y * y[t + u][3];
-                m0 = fmaxf(m0, fmaxf(fabsf(r[t + u][0]), fabsf(r[t + u][1])));
-                m1 = fmaxf(m1, fmaxf(fabsf(r[t + u][2]), fabsf(r[t + u][3])));
-            }
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t v0 = v[t >> 1][2 * (t & 1)], v1 = v[t >> 1][2 * (t & 1) + 1];
+            r[t][0] = __uint_as_float(v0 << 16) - ck[t].x * y[t][0];
+            r[t][1] = __uint_as_float(v0 & 0xffff0000u) - ck[t].y * y[t][1];
+            r[t][2] = __uint_as_float(v1 << 16) - ck[t].x * y[t][2];
+            r[t][3] = __uint_as_float(v1 & 0xffff0000u) - ck[t].y * y[t][3];
+            m0 = fmaxf(m0, fmaxf(fabsf(r[t][0]), fabsf(r[t][1])));
+            m1 = fmaxf(m1, fmaxf(fabsf(r[t][2]), fabsf(r[t][3])));
         }
         // N^T = R^T X^T: three of the four products of the split operands
         float nn[4][4], nl[4][4];
@@ -297,15 +340,13 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, false, !REC, 24>::WARPS
                 split_half(r[2 * ks + 1][2] * fr1, r[2 * ks + 1][3] * fr1, hi[3], lo[3]);
 #pragma unroll
                 for (int half = ks; half < 2; ++half) {   // X is zero above the diagonal
-                    uint32_t xh[4], xl[4];
-                    ldsm4(xh, sb + L::XH + (16 * half + nrow) * L::XP + ncol + ks * 32);
-                    ldsm4(xl, sb + L::XL + (16 * half + nrow) * L::XP + ncol + ks * 32);
-                    mma16816(nn[2 * half], hi, xh[0], xh[1]);
-                    mma16816(nn[2 * half + 1], hi, xh[2], xh[3]);
-                    mma16816(nl[2 * half], lo, xh[0], xh[1]);
-                    mma16816(nl[2 * half + 1], lo, xh[2], xh[3]);
-                    mma16816(nl[2 * half], hi, xl[0], xl[1]);
-                    mma16816(nl[2 * half + 1], hi, xl[2], xl[3]);
+                    const uint32_t(&h4)[4] = xh[half + ks], (&l4)[4] = xl[half + ks];
+                    mma16816(nn[2 * half], hi, h4[0], h4[1]);
+                    mma16816(nn[2 * half + 1], hi, h4[2], h4[3]);
+                    mma16816(nl[2 * half], lo, h4[0], h4[1]);
+                    mma16816(nl[2 * half + 1], lo, h4[2], h4[3]);
+                    mma16816(nl[2 * half], hi, l4[0], l4[1]);
+                    mma16816(nl[2 * half + 1], hi, l4[2], l4[3]);
                 }
             }
 #pragma unroll
@@ -317,7 +358,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, false, !REC, 24>::WARPS
             }
         }
         if (REC) {
-            float *dst = a.n_out + (row * a.H + h) * a.dv + j0 + jr;
+            float *dst = args.n_out + (row * a.H + h) * a.dv + j0 + jr;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -331,14 +372,12 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, false, !REC, 24>::WARPS
         m0 = m1 = 0.f;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const float2 b = *reinterpret_cast<const float2 *>(scal + L::BETA * kChunk + 8 * t + tc);
             const float2 e = *reinterpret_cast<const float2 *>(scal + L::OK * kChunk + 8 * t + tc);
-            const float2 k = *reinterpret_cast<const float2 *>(scal + L::IK * kChunk + 8 * t + tc);
+            const float2 k = *reinterpret_cast<const float2 *>(scal + L::BK * kChunk + 8 * t + tc);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float u = nn[t][x] * ((x & 1) ? b.y : b.x);
-                r[t][x] = u * ((x & 1) ? e.y : e.x);
-                nn[t][x] = u * ((x & 1) ? k.y : k.x);
+                r[t][x] = nn[t][x] * ((x & 1) ? e.y : e.x);
+                nn[t][x] *= (x & 1) ? k.y : k.x;
             }
             m0 = fmaxf(m0, fmaxf(fabsf(r[t][0]), fabsf(r[t][1])));
             m1 = fmaxf(m1, fmaxf(fabsf(r[t][2]), fabsf(r[t][3])));
@@ -391,95 +430,78 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, CL, false, !REC, 24>::WARPS
                 }
             }
         }
-        if (!REC) {
+        if (!REC && (KS == 1 || part == 0)) {
             const float fu0 = row_scale(quad_max(m2), out.i0), fu1 = row_scale(quad_max(m3), out.i1);
-            const int t0 = KS == 2 ? part * 16 : 0;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 out.u[ks][0] = pack_half(nn[2 * ks][0] * fu0, nn[2 * ks][1] * fu0);
                 out.u[ks][1] = pack_half(nn[2 * ks][2] * fu1, nn[2 * ks][3] * fu1);
                 out.u[ks][2] = pack_half(nn[2 * ks + 1][0] * fu0, nn[2 * ks + 1][1] * fu0);
                 out.u[ks][3] = pack_half(nn[2 * ks + 1][2] * fu1, nn[2 * ks + 1][3] * fu1);
+                if (KS == 2)
+                    hand[kHandU / 16 + ks * 32] = make_uint4(out.u[ks][0], out.u[ks][1], out.u[ks][2], out.u[ks][3]);
             }
-            const uint32_t pb = sb + L::P + nrow * L::XP + ncol;
-            if constexpr (KS == 2) {
-                ldsm4(out.p[0], pb + t0 * L::XP);
-                if (part) {
-                    ldsm4(out.p[1], pb + t0 * L::XP + 32);
-                } else {
+            if (KS == 2)
+                reinterpret_cast<float2 *>(pipe.hand(group, ci & 1) + kHandScale)[lane] = make_float2(out.i0, out.i1);
+        }
+        if (!REC && KS == 1) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) out.p[1][x] = 0u;
-                }
-            } else {
-                ldsm4(out.p[0], pb);
-                ldsm4(out.p[1], pb + 16 * L::XP);
-                ldsm4(out.p[2], pb + 16 * L::XP + 32);
-            }
-#pragma unroll
-            for (int t = 0; t < 4 / KS; ++t) {
-                out.cq[t] = *reinterpret_cast<const float2 *>(scal + L::CQ * kChunk + t0 + 8 * t + tc);
-                out.iq[t] = *reinterpret_cast<const float2 *>(scal + L::IQ * kChunk + t0 + 8 * t + tc);
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) out.oq[t][x] = oq[t][x];
-            }
-            if (KS == 1 || ci + 1 == chunks)
-                out.write(out_tile, M::OP, a.o + (row * a.H + h) * a.dv + j0, vstride, part, valid);
+            out.template read_stage<L>(sb, scal);
+            out.write(out_tile, M::OP, args.o + (row * a.H + h) * a.dv + j0, vstride, valid);
         }
         pipe.release(st);
+        if (!REC && KS == 2 && lane == 0) mbar_arrive(pipe.handed + group * 2 + (ci & 1));
     }
-    if (ok && a.state_out) {
-        float *dst = a.state_out + state_off;
+    if (ok && args.state_out) {
+        float *dst = args.state_out + state_off;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 dst[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] = s[i][x];
     }
-    pipe.finish();
 }
 
-template <int DK, int NCW, int KS, int CL, bool REC>
-static cudaError_t launch_chain_t(const ChainArgs &a, int64_t units, cudaStream_t st) {
-    using M = Pipe<DK, NCW, KS, CL, false, !REC, 24>;
-    return launch_pipe(gdr_chain_kernel<DK, NCW, KS, CL, REC>, a, a.k, a.q, a.v, a.rows, DK, M::W,
-                       units * CL, M::WARPS * 32, M::BYTES, CL, st);
+template <int DK, int NCW, int KS, bool REC>
+static cudaError_t launch_chain_t(const ChainArgs &a, const void *v, int64_t rows, int64_t units, cudaStream_t st) {
+    using M = Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS, REC>()>;
+    return launch_chain_kernel(gdr_chain_kernel<DK, NCW, KS, REC>, a, v, rows, M::W, units, M::WARPS * 32, M::BYTES,
+                               st);
 }
 
-// Columns per CTA and warps per column group.  The chain's rate is set by its warps'
-// matrix instructions (8 cycles each per SM quarter), so with few (sequence, head) units
-// the work is spread over as many SMs and warps as there are; with many, one CTA takes all
-// columns, so that the producers' work is done once per chunk without a cluster.
+// Columns per CTA and warps per column group.  The chain's rate is set by its warps' matrix
+// instructions (8 cycles each per SM quarter) and their latency, so with few (sequence, head)
+// units the work is spread over as many SMs and warps as there are; with many, one CTA takes all
+// columns and loads each chunk once.
 template <int DK, bool REC>
-static cudaError_t launch_chain_d(const ChainArgs &a, int64_t units, cudaStream_t st) {
-    if (a.dv == 128) {
-        if (units * 4 <= 128) return launch_chain_t<DK, 2, 2, 4, REC>(a, units, st);
-        if (units * 2 <= 148) return launch_chain_t<DK, 4, 1, 2, REC>(a, units, st);
-        return launch_chain_t<DK, 8, 1, 1, REC>(a, units, st);
-    }
-    if (units * 2 <= 148) return launch_chain_t<DK, 2, 2, 2, REC>(a, units, st);
-    return launch_chain_t<DK, 4, 1, 1, REC>(a, units, st);
+static cudaError_t launch_chain_d(const ChainArgs &a, const void *v, int64_t rows, int64_t units, cudaStream_t st) {
+    if (units * (a.in.dv / 32) <= 148) return launch_chain_t<DK, 2, 2, REC>(a, v, rows, units, st);
+    if (units * (a.in.dv / 64) <= 148 || a.in.dv == 64) return launch_chain_t<DK, 4, 1, REC>(a, v, rows, units, st);
+    return launch_chain_t<DK, 8, 1, REC>(a, v, rows, units, st);
 }
 
 }  // namespace gdr
 
-cudaError_t launch_gdr_prefill(const GdrArgs &p, cudaStream_t st) {
-    using bf = __nv_bfloat16;
-    gdr::ChainArgs a{(const bf *)p.q, (const bf *)p.k, (const bf *)p.v, (const bf *)p.g,
-                     (const bf *)p.beta, p.state_in, p.cu_seqlens, p.T, p.rows, p.Hk, p.H, p.dv,
-                     (bf *)p.o, p.state_out, nullptr, nullptr, nullptr, nullptr, p.err, p.epoch};
+cudaError_t launch_gdr_prefill(const GdrArgs &p, void *workspace, cudaStream_t st) {
+    const GdrImages m = gdr_images(workspace, p.rows, p.N, p.Hk, p.H, p.dk, false);
+    const cudaError_t e = launch_gdr_prep(p, m, st);
+    if (e != cudaSuccess) return e;
+    gdr::ChainArgs a{{m.keys, m.forward, p.cu_seqlens, p.T, p.Hk, p.H, p.dv, p.err, p.epoch},
+                     p.state_in, (__nv_bfloat16 *)p.o, p.state_out};
     const int64_t units = (int64_t)p.N * p.H;
-    return p.dk == 64 ? gdr::launch_chain_d<64, false>(a, units, st)
-                      : gdr::launch_chain_d<128, false>(a, units, st);
+    return p.dk == 64 ? gdr::launch_chain_d<64, false>(a, p.v, p.rows, units, st)
+                      : gdr::launch_chain_d<128, false>(a, p.v, p.rows, units, st);
 }
 
-cudaError_t launch_gdr_recompute(const GdrArgs &p, const GdrBackwardSpace &w, cudaStream_t st) {
-    using bf = __nv_bfloat16;
-    gdr::ChainArgs a{(const bf *)p.q, (const bf *)p.k, (const bf *)p.v, (const bf *)p.g,
-                     (const bf *)p.beta, p.state_in, p.cu_seqlens, p.T, p.rows, p.Hk, p.H, p.dv,
-                     nullptr, nullptr, w.n, w.s_blocks, w.s_tops, w.owners, p.err, p.epoch};
+cudaError_t launch_gdr_recompute(const GdrArgs &p, const GdrImages &m, const GdrBackwardSpace &w, cudaStream_t st) {
+    gdr::ChainArgs a{{m.keys, m.forward, p.cu_seqlens, p.T, p.Hk, p.H, p.dv, p.err, p.epoch},
+                     p.state_in, nullptr, nullptr, w.n, w.s_blocks, w.s_tops, w.owners};
     const int64_t units = (int64_t)p.N * p.H;
-    return p.dk == 64 ? gdr::launch_chain_d<64, true>(a, units, st)
-                      : gdr::launch_chain_d<128, true>(a, units, st);
+    return p.dk == 64 ? gdr::launch_chain_d<64, true>(a, p.v, p.rows, units, st)
+                      : gdr::launch_chain_d<128, true>(a, p.v, p.rows, units, st);
 }
 
 }  // namespace kda

@@ -18,10 +18,18 @@ struct GdrArgs {
     uint32_t epoch;
 };
 
-// bf16, tensor cores
-cudaError_t launch_gdr_prefill(const GdrArgs &a, cudaStream_t st);
+// bf16, tensor cores.  Images of the chunks (gdr_prep.cu) in the caller's workspace, 256-byte
+// aligned: keys and queries, the forward's inverses, and the adjoint's for a backward.
+struct GdrImages {
+    unsigned char *keys, *forward, *adjoint;
+};
+size_t gdr_image_bytes(int64_t rows, int N, int Hk, int H, int dk, bool adjoint);
+GdrImages gdr_images(void *space, int64_t rows, int N, int Hk, int H, int dk, bool adjoint);
+cudaError_t launch_gdr_prep(const GdrArgs &a, const GdrImages &m, cudaStream_t st);
+// workspace: gdr_image_bytes(.., false)
+cudaError_t launch_gdr_prefill(const GdrArgs &a, void *workspace, cudaStream_t st);
 
-// Backward, bf16.  Three kernels: the forward's chain again, keeping N and the state before
+// Backward, bf16.  The images, then three kernels: the forward's chain again, keeping N and the state before
 // each 64-token block; the adjoint chain, keeping E and the adjoint state behind each block;
 // the gradients of each block (gdr_backward.cu).
 struct GdrBackwardSpace {
@@ -36,8 +44,9 @@ struct GdrGrads {
     void *dq, *dk, *dv, *dg, *dbeta;
     float *dstate_in;              // or nullptr
 };
-size_t gdr_backward_workspace_bytes(int64_t rows, int N, int H, int dk, int dv, bool bf16);
-cudaError_t launch_gdr_recompute(const GdrArgs &a, const GdrBackwardSpace &w, cudaStream_t st);
+size_t gdr_backward_workspace_bytes(int64_t rows, int N, int Hk, int H, int dk, int dv, bool bf16);
+cudaError_t launch_gdr_recompute(const GdrArgs &a, const GdrImages &m, const GdrBackwardSpace &w,
+                                 cudaStream_t st);
 // workspace: gdr_backward_workspace_bytes bytes, 256-byte aligned
 cudaError_t launch_gdr_backward(const GdrArgs &a, const GdrGrads &g, int64_t rows, bool bf16,
                                 void *workspace, cudaStream_t st);

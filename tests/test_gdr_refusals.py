@@ -16,7 +16,7 @@ def lib():
 
 def prefill(lib, **kw):
     a = dict(q=16, k=32, v=48, g=64, beta=80, state_in=None, cu=None, B=1, T=16, N=1, Hk=2, H=4, dk=128, dv=128,
-             dtype=binding.KDA_BF16, o=96, state_out=None, stream=None)
+             dtype=binding.KDA_BF16, o=96, state_out=None, workspace=256, workspace_bytes=1 << 40, stream=None)
     a.update(kw)
     return lib.kda_gdr_chunk_prefill(*a.values())
 
@@ -24,7 +24,8 @@ def prefill(lib, **kw):
 @pytest.mark.parametrize("bad", [
     dict(B=-1), dict(T=-1), dict(N=-1), dict(N=2), dict(Hk=0), dict(H=0), dict(Hk=3), dict(dk=0), dict(dv=-64),
     dict(dtype=2), dict(cu=4, B=2, N=2), dict(q=None), dict(k=None), dict(v=None), dict(g=None), dict(beta=None),
-    dict(o=None), dict(q=17), dict(k=40), dict(v=8), dict(o=100), dict(state_in=4), dict(state_out=8)])
+    dict(o=None), dict(q=17), dict(k=40), dict(v=8), dict(o=100), dict(state_in=4), dict(state_out=8),
+    dict(workspace=None), dict(workspace=272), dict(workspace_bytes=100)])
 def test_prefill_refuses(lib, bad):
     assert prefill(lib, **bad) == BAD
 
@@ -33,6 +34,14 @@ def test_prefill_refuses(lib, bad):
                                  dict(cu=4, N=2 ** 28)])
 def test_prefill_does_not_support(lib, bad):
     assert prefill(lib, **bad) == NOT
+
+
+def test_prefill_workspace(lib):
+    f = lib.kda_gdr_prefill_workspace_bytes
+    need = f(100, 2, 2, 4, 128, 64, binding.KDA_BF16)
+    assert need > 0 and need % 256 == 0 and f(100, 3, 2, 4, 128, 64, binding.KDA_BF16) > need
+    assert f(100, 2, 2, 4, 128, 64, binding.KDA_F32) == 0 and f(100, 2, 3, 4, 128, 64, binding.KDA_BF16) == 0
+    assert prefill(lib, workspace_bytes=f(16, 1, 2, 4, 128, 128, binding.KDA_BF16) - 1) == BAD
 
 
 def test_prefill_of_nothing(lib):
