@@ -56,7 +56,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slices = a.dv / W;
     const int slice = blockIdx.x % slices, unit = blockIdx.x / slices;
-    const int h = unit % a.H, n = unit / a.H, hk = h / (a.H / a.Hk);
+    const int h = unit % a.H, n = a.order ? a.order[unit / a.H] : unit / a.H, hk = h / (a.H / a.Hk);
     const Span span = sequence_span(a.cu, n, a.T);
     const int chunks = (span.len + kChunk - 1) / kChunk;
     const M pipe(smem, a.err, a.epoch);
@@ -850,13 +850,13 @@ cudaError_t launch_gdr_backward(const GdrArgs &p, const GdrGrads &g, int64_t row
     s.owners = reinterpret_cast<int32_t *>(take(slots / p.H * 4));
     cudaError_t e = cudaMemsetAsync(s.owners, 0xff, slots / p.H * 4, st);
     if (e != cudaSuccess) return e;
-    const GdrImages m = gdr_images(w, rows, p.N, p.Hk, p.H, p.dk, true);
+    const GdrImages m = gdr_images(w, p, true);
     e = launch_gdr_prep(p, m, st);
     if (e != cudaSuccess) return e;
     e = launch_gdr_recompute(p, m, s, st);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)p.N * p.H;
-    AdjointArgs a{{m.keys, m.adjoint, p.cu_seqlens, p.T, p.Hk, p.H, p.dv, p.err, p.epoch},
+    AdjointArgs a{{m.keys, m.adjoint, p.cu_seqlens, m.order, p.T, p.Hk, p.H, p.dv, p.err, p.epoch},
                   g.dstate_out, (bf *)g.dv, g.dstate_in, s.e, s.z_blocks, s.z_tops};
     e = p.dk == 64 ? launch_adjoint_d<64>(a, g.dout, rows, units, st) : launch_adjoint_d<128>(a, g.dout, rows, units, st);
     if (e != cudaSuccess) return e;

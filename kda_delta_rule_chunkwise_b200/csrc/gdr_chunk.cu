@@ -48,6 +48,23 @@ struct ChunkOut {
     float oq[4][4], i0, i1;
     float2 cq[4], iq[4];
 
+    // U^T times ik, fp16 after a power-of-two scale per column
+    __device__ __forceinline__ void pack_u(const float (&x)[4][4]) {
+        float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            m0 = fmaxf(m0, fmaxf(fabsf(x[t][0]), fabsf(x[t][1])));
+            m1 = fmaxf(m1, fmaxf(fabsf(x[t][2]), fabsf(x[t][3])));
+        }
+        const float f0 = row_scale(quad_max(m0), i0), f1 = row_scale(quad_max(m1), i1);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            u[ks][0] = pack_half(x[2 * ks][0] * f0, x[2 * ks][1] * f0);
+            u[ks][1] = pack_half(x[2 * ks][2] * f1, x[2 * ks][3] * f1);
+            u[ks][2] = pack_half(x[2 * ks + 1][0] * f0, x[2 * ks + 1][1] * f0);
+            u[ks][3] = pack_half(x[2 * ks + 1][2] * f1, x[2 * ks + 1][3] * f1);
+        }
+    }
     // P and the row scalars of the chunk in a stage
     template <typename L>
     __device__ __forceinline__ void read_stage(uint32_t sb, const float *scal) {
@@ -103,9 +120,8 @@ struct ChunkOut {
     }
 };
 // The hand-over of a chunk from a group's two chain warps to its output warp (KS = 2): per lane the
-// two partial Q S (4 float4 each), U^T as packed and its two scales.
-constexpr int kHandOq = 0, kHandU = 2 * 4 * 512, kHandScale = kHandU + 2 * 512;
-constexpr int kHandBytes = kHandScale + 256;
+// two partial Q S (4 float4 each) and U^T (4 float4, each warp writes its half of the tokens).
+constexpr int kHandU = 2 * 4 * 512, kHandBytes = kHandU + 4 * 512;
 template <int KS, bool REC>
 constexpr int hand_bytes() { return KS == 2 && !REC ? kHandBytes : 0; }
 
@@ -124,7 +140,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slices = a.dv / W;
     const int slice = blockIdx.x % slices, unit = blockIdx.x / slices;
-    const int h = unit % a.H, n = unit / a.H, hk = h / (a.H / a.Hk);
+    const int h = unit % a.H, n = a.order ? a.order[unit / a.H] : unit / a.H, hk = h / (a.H / a.Hk);
     const Span span = sequence_span(a.cu, n, a.T);
     const int chunks = (span.len + kChunk - 1) / kChunk;
     if (REC && h == 0 && slice == 0)
@@ -138,30 +154,22 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
         unsigned char *tile = smem + M::OUT + group * kChunk * M::OP;
         ChunkOut out;
         for (int ci = 0; ci < chunks; ++ci) {
-            const int st = ci % M::ST, b = ci & 1;
-            const uint32_t turn = (ci >> 1) & 1;
-            if (!pipe.wait(pipe.full + st, (ci / M::ST) & 1)) break;
+            const int st = ci % M::ST;
+            const uint32_t turn = (ci / M::ST) & 1;
+            if (!pipe.wait(pipe.full + st, turn)) break;
             out.template read_stage<L>(smem_u32(pipe.stage(st)),
                                        reinterpret_cast<const float *>(pipe.stage(st) + L::S));
-            if (!pipe.wait(pipe.handed + group * 2 + b, turn)) break;
-            const unsigned char *hand = pipe.hand(group, b);
-            const float4 *oq = reinterpret_cast<const float4 *>(hand + kHandOq) + lane;
+            if (!pipe.wait(pipe.handed + group * M::ST + st, turn)) break;
+            const float4 *hand = reinterpret_cast<const float4 *>(pipe.hand(group, st)) + lane;
+            float u[4][4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const float4 x = oq[t * 32], y = oq[(4 + t) * 32];
+                const float4 x = hand[t * 32], y = hand[(4 + t) * 32], w = hand[(8 + t) * 32];
                 out.oq[t][0] = x.x + y.x; out.oq[t][1] = x.y + y.y;
                 out.oq[t][2] = x.z + y.z; out.oq[t][3] = x.w + y.w;
+                u[t][0] = w.x; u[t][1] = w.y; u[t][2] = w.z; u[t][3] = w.w;
             }
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const uint4 w = reinterpret_cast<const uint4 *>(hand + kHandU)[ks * 32 + lane];
-                out.u[ks][0] = w.x; out.u[ks][1] = w.y; out.u[ks][2] = w.z; out.u[ks][3] = w.w;
-            }
-            const float2 sc = reinterpret_cast<const float2 *>(hand + kHandScale)[lane];
-            out.i0 = sc.x;
-            out.i1 = sc.y;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pipe.taken + group * 2 + b);
+            out.pack_u(u);
             const int64_t row = span.row + (int64_t)ci * kChunk;
             out.write(tile, M::OP, args.o + (row * a.H + h) * a.dv + slice * W + group * 16,
                       (int64_t)a.H * a.dv, span.len - ci * kChunk);
@@ -261,7 +269,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
             y[t][0] *= is0; y[t][1] *= is0; y[t][2] *= is1; y[t][3] *= is1;
             oq[t][0] *= is0; oq[t][1] *= is0; oq[t][2] *= is1; oq[t][3] *= is1;
         }
-        uint4 *hand = KS == 2 && !REC ? reinterpret_cast<uint4 *>(pipe.hand(group, ci & 1)) + lane : nullptr;
+        float4 *hand = KS == 2 && !REC ? reinterpret_cast<float4 *>(pipe.hand(group, st)) + lane : nullptr;
         if (KS == 2) {
             // add the other half's sums.  Buffers alternate: the other warp has read the ones of
             // two chunks before by now.
@@ -271,14 +279,10 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
             for (int t = 0; t < 4; ++t) mine[t * 32] = make_float4(y[t][0], y[t][1], y[t][2], y[t][3]);
             __syncwarp();
             if (lane == 0) mbar_arrive(pipe.swapped + group * 2 + (part ^ 1));
-            if (!REC) {   // this half's Q S to the output warp, which has taken the one of two chunks before
-                ok = ci < 2 || pipe.wait(pipe.taken + group * 2 + (ci & 1), ((ci >> 1) - 1) & 1);
-                if (!ok) break;
+            if (!REC)   // this half's Q S to the output warp
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
-                    reinterpret_cast<float4 *>(hand)[(part * 4 + t) * 32] =
-                        make_float4(oq[t][0], oq[t][1], oq[t][2], oq[t][3]);
-            }
+                    hand[(part * 4 + t) * 32] = make_float4(oq[t][0], oq[t][1], oq[t][2], oq[t][3]);
         }
         // what does not depend on the other half, while it is on its way
         uint32_t v[2][4], xh[3][4], xl[3][4];   // values; blocks (0,0) (1,0) (1,1) of X
@@ -368,21 +372,27 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
                 }
         }
         // U = beta N in the scaled units of K', and with the decay to the chunk's end
-        float m2 = 0.f, m3 = 0.f;
         m0 = m1 = 0.f;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const float2 e = *reinterpret_cast<const float2 *>(scal + L::OK * kChunk + 8 * t + tc);
-            const float2 k = *reinterpret_cast<const float2 *>(scal + L::BK * kChunk + 8 * t + tc);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                r[t][x] = nn[t][x] * ((x & 1) ? e.y : e.x);
-                nn[t][x] *= (x & 1) ? k.y : k.x;
-            }
+            for (int x = 0; x < 4; ++x) r[t][x] = nn[t][x] * ((x & 1) ? e.y : e.x);
             m0 = fmaxf(m0, fmaxf(fabsf(r[t][0]), fabsf(r[t][1])));
             m1 = fmaxf(m1, fmaxf(fabsf(r[t][2]), fabsf(r[t][3])));
-            m2 = fmaxf(m2, fmaxf(fabsf(nn[t][0]), fabsf(nn[t][1])));
-            m3 = fmaxf(m3, fmaxf(fabsf(nn[t][2]), fabsf(nn[t][3])));
+        }
+        if (!REC)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const float2 k = *reinterpret_cast<const float2 *>(scal + L::BK * kChunk + 8 * t + tc);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) nn[t][x] *= (x & 1) ? k.y : k.x;
+                if (KS == 2 && t / 2 == part)
+                    hand[(8 + t) * 32] = make_float4(nn[t][0], nn[t][1], nn[t][2], nn[t][3]);
+            }
+        if (KS == 2 && !REC) {   // the output warp may go on
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pipe.handed + group * M::ST + st);
         }
         // S' = Gamma_C S + (decayed U)^T K'
         {
@@ -430,21 +440,8 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
                 }
             }
         }
-        if (!REC && (KS == 1 || part == 0)) {
-            const float fu0 = row_scale(quad_max(m2), out.i0), fu1 = row_scale(quad_max(m3), out.i1);
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                out.u[ks][0] = pack_half(nn[2 * ks][0] * fu0, nn[2 * ks][1] * fu0);
-                out.u[ks][1] = pack_half(nn[2 * ks][2] * fu1, nn[2 * ks][3] * fu1);
-                out.u[ks][2] = pack_half(nn[2 * ks + 1][0] * fu0, nn[2 * ks + 1][1] * fu0);
-                out.u[ks][3] = pack_half(nn[2 * ks + 1][2] * fu1, nn[2 * ks + 1][3] * fu1);
-                if (KS == 2)
-                    hand[kHandU / 16 + ks * 32] = make_uint4(out.u[ks][0], out.u[ks][1], out.u[ks][2], out.u[ks][3]);
-            }
-            if (KS == 2)
-                reinterpret_cast<float2 *>(pipe.hand(group, ci & 1) + kHandScale)[lane] = make_float2(out.i0, out.i1);
-        }
         if (!REC && KS == 1) {
+            out.pack_u(nn);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -453,7 +450,6 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
             out.write(out_tile, M::OP, args.o + (row * a.H + h) * a.dv + j0, vstride, valid);
         }
         pipe.release(st);
-        if (!REC && KS == 2 && lane == 0) mbar_arrive(pipe.handed + group * 2 + (ci & 1));
     }
     if (ok && args.state_out) {
         float *dst = args.state_out + state_off;
@@ -486,10 +482,10 @@ static cudaError_t launch_chain_d(const ChainArgs &a, const void *v, int64_t row
 }  // namespace gdr
 
 cudaError_t launch_gdr_prefill(const GdrArgs &p, void *workspace, cudaStream_t st) {
-    const GdrImages m = gdr_images(workspace, p.rows, p.N, p.Hk, p.H, p.dk, false);
+    const GdrImages m = gdr_images(workspace, p, false);
     const cudaError_t e = launch_gdr_prep(p, m, st);
     if (e != cudaSuccess) return e;
-    gdr::ChainArgs a{{m.keys, m.forward, p.cu_seqlens, p.T, p.Hk, p.H, p.dv, p.err, p.epoch},
+    gdr::ChainArgs a{{m.keys, m.forward, p.cu_seqlens, m.order, p.T, p.Hk, p.H, p.dv, p.err, p.epoch},
                      p.state_in, (__nv_bfloat16 *)p.o, p.state_out};
     const int64_t units = (int64_t)p.N * p.H;
     return p.dk == 64 ? gdr::launch_chain_d<64, false>(a, p.v, p.rows, units, st)
@@ -497,7 +493,7 @@ cudaError_t launch_gdr_prefill(const GdrArgs &p, void *workspace, cudaStream_t s
 }
 
 cudaError_t launch_gdr_recompute(const GdrArgs &p, const GdrImages &m, const GdrBackwardSpace &w, cudaStream_t st) {
-    gdr::ChainArgs a{{m.keys, m.forward, p.cu_seqlens, p.T, p.Hk, p.H, p.dv, p.err, p.epoch},
+    gdr::ChainArgs a{{m.keys, m.forward, p.cu_seqlens, m.order, p.T, p.Hk, p.H, p.dv, p.err, p.epoch},
                      p.state_in, nullptr, nullptr, w.n, w.s_blocks, w.s_tops, w.owners};
     const int64_t units = (int64_t)p.N * p.H;
     return p.dk == 64 ? gdr::launch_chain_d<64, true>(a, p.v, p.rows, units, st)

@@ -247,7 +247,7 @@ __device__ __forceinline__ void gram_lower(float (&acc)[6][4], uint32_t m, uint3
 // What both chain kernels get.
 struct ChainInput {
     const unsigned char *keys, *heads;   // images: [chunk_slots, Hk], [chunk_slots, H]
-    const int32_t *cu;
+    const int32_t *cu, *order;           // order: sequences from the longest, or nullptr
     int64_t T;
     int Hk, H, dv;
     uint32_t *err;
@@ -256,8 +256,8 @@ struct ChainInput {
 
 // NCW groups of 16 value columns per CTA, KS warps per group (each with dk / KS channels).  A loader
 // warp copies chunk after chunk into a ring of ST stages: two images and a box of the values.  With
-// OUTW > 0 an output warp per group finishes what the chain leaves it (OUTW bytes a chunk and group,
-// in two buffers).
+// OUTW > 0 an output warp per group finishes what the chain leaves it, OUTW bytes a chunk and group in
+// a buffer per stage (so that a full stage's buffer is free: the output warp has released it too).
 //
 // The chain warps' loop is long straight code (about 20 KiB); what runs beside it on an SM has to
 // be little, or the warps wait for instructions.  (The chunks' images were made here first, by
@@ -273,30 +273,27 @@ struct Pipe {
     static constexpr int OUT = ST * L::BYTES;
     static constexpr int SWAP = OUT + NCW * kChunk * OP;
     static constexpr int HAND = SWAP + (KS == 2 ? NCW * 2 * 2 * 16 * 32 * 4 : 0);
-    static constexpr int BARS = HAND + OW * 2 * OUTW;
-    static constexpr int BYTES = BARS + (2 * ST + 6 * NCW) * 8 + 16;
+    static constexpr int BARS = HAND + OW * ST * OUTW;
+    static constexpr int BYTES = BARS + (2 * ST + 2 * NCW + OW * ST) * 8 + 16;
     static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 
     unsigned char *smem;
-    uint64_t *full, *empty, *swapped, *handed, *taken;
+    uint64_t *full, *empty, *swapped, *handed;
     volatile uint32_t *abort;
     uint32_t *err;
     uint32_t epoch;
 
     __device__ __forceinline__ Pipe(unsigned char *s, uint32_t *e, uint32_t ep) : smem(s), err(e), epoch(ep) {
         full = reinterpret_cast<uint64_t *>(smem + BARS);
-        empty = full + ST, swapped = empty + ST, handed = swapped + 2 * NCW, taken = handed + 2 * NCW;
-        abort = reinterpret_cast<volatile uint32_t *>(taken + 2 * NCW);
+        empty = full + ST, swapped = empty + ST, handed = swapped + 2 * NCW;
+        abort = reinterpret_cast<volatile uint32_t *>(handed + OW * ST);
         if (threadIdx.x == 0) {
             for (int i = 0; i < ST; ++i) {
                 mbar_init(full + i, 1);
                 mbar_init(empty + i, CHAIN + OW);
             }
-            for (int i = 0; i < 2 * NCW; ++i) {
-                mbar_init(swapped + i, 1);
-                mbar_init(handed + i, KS);
-                mbar_init(taken + i, 1);
-            }
+            for (int i = 0; i < 2 * NCW; ++i) mbar_init(swapped + i, 1);
+            for (int i = 0; i < OW * ST; ++i) mbar_init(handed + i, KS);
             mbar_fence_init();
             *abort = 0u;
         }
@@ -306,9 +303,9 @@ struct Pipe {
         return warp_wait(bar, parity, err, epoch, abort);
     }
     __device__ __forceinline__ unsigned char *stage(int i) const { return smem + i * L::BYTES; }
-    // buffer b of a group's hand-over to its output warp
-    __device__ __forceinline__ unsigned char *hand(int group, int b) const {
-        return smem + HAND + (group * 2 + b) * OUTW;
+    // stage s of a group's hand-over to its output warp
+    __device__ __forceinline__ unsigned char *hand(int group, int s) const {
+        return smem + HAND + (group * ST + s) * OUTW;
     }
 
     // The loader warp.  REVERSE: the sequence's chunks from the last to the first.

@@ -22,9 +22,10 @@ struct GdrArgs {
 // aligned: keys and queries, the forward's inverses, and the adjoint's for a backward.
 struct GdrImages {
     unsigned char *keys, *forward, *adjoint;
+    int32_t *order;   // packed sequences from the longest to the shortest, or nullptr (N = 1, dense)
 };
 size_t gdr_image_bytes(int64_t rows, int N, int Hk, int H, int dk, bool adjoint);
-GdrImages gdr_images(void *space, int64_t rows, int N, int Hk, int H, int dk, bool adjoint);
+GdrImages gdr_images(void *space, const GdrArgs &a, bool adjoint);
 cudaError_t launch_gdr_prep(const GdrArgs &a, const GdrImages &m, cudaStream_t st);
 // workspace: gdr_image_bytes(.., false)
 cudaError_t launch_gdr_prefill(const GdrArgs &a, void *workspace, cudaStream_t st);

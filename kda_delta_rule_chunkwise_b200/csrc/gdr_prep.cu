@@ -30,42 +30,59 @@ struct PrepArgs {
     unsigned char *keys, *forward, *adjoint;
 };
 
-constexpr int kPrepWarps = 6;
-constexpr int kAP = 20;                    // fp32 row pitch of a diagonal block of A
-constexpr int kPrepScratch = 2 * 16 * kAP * 4;
+template <bool ADJ>
+constexpr int prep_warps() { return ADJ ? 6 : 8; }   // as many as their tiles fit
+// The diagonal blocks of A while they are inverted stand where P of the image will: 2 x 16 rows.
+constexpr int kAP = 20;   // fp32 row pitch
+static_assert(2 * 16 * kAP * 4 <= kChunk * HeadImage<false>::XP, "A fits the place of P");
 // The forward's image; the backward's recomputation has no use for P.
 template <bool ADJ>
 constexpr int forward_bytes() { return ADJ ? HeadImage<false>::P : HeadImage<false>::BYTES; }
 template <int DK, bool ADJ>
 constexpr int prep_warp_bytes() {
-    return KeyImage<DK>::BYTES + kPrepScratch + forward_bytes<ADJ>() + (ADJ ? HeadImage<true>::BYTES : 0);
+    return KeyImage<DK>::BYTES + forward_bytes<ADJ>() + (ADJ ? HeadImage<true>::BYTES : 0);
 }
 
-// Lane r scales row r (zeros unless `valid`) into a padded fp16 tile; returns 2^-e.
+// 32 rows of D bf16 elements into a padded tile, zeros from row `valid` on: coalesced copies.
 template <int D>
-__device__ __forceinline__ float scale_row(const __nv_bfloat16 *src, uint32_t tile, int pitch, bool valid) {
-    uint4 w[D / 8];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (valid) w[i] = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+__device__ __forceinline__ void copy_rows(uint32_t tile, int pitch, const __nv_bfloat16 *base, int64_t stride,
+                                          int valid) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR;
+    const int lane = threadIdx.x & 31, c = lane % LPR;
+#pragma unroll 4
+    for (int r = lane / LPR; r < kChunk; r += RPI) {
+        const bool ok = r < valid;
+        const int n = ok ? 16 : 0;   // the rest of the 16 bytes is filled with zeros
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + r * pitch + c * 16),
+                     "l"(base + (ok ? r * stride : 0) + c * 8), "r"(n)
+                     : "memory");
     }
+}
+// In place: lane r scales row r of a bf16 tile into fp16; returns 2^-e.
+template <int D>
+__device__ __forceinline__ float scale_row(uint32_t tile, int pitch) {
+    tile += (threadIdx.x & 31) * pitch;
+    uint32_t w[D / 8][4];
     __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
-        for (uint32_t u : {w[i].x, w[i].y, w[i].z, w[i].w})
-            m = __hmax2(m, __habs2(reinterpret_cast<const __nv_bfloat162 &>(u)));
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                     : "r"(tile + i * 16)
+                     : "memory");
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = __hmax2(m, __habs2(reinterpret_cast<const __nv_bfloat162 &>(w[i][j])));
     const float top = fmaxf(__low2float(m), __high2float(m));
     const int e = min(max((int)(__float_as_uint(top) >> 23), 1), 253);
     const float sc = __uint_as_float((uint32_t)(254 - e) << 23);
-    tile += (threadIdx.x & 31) * pitch;
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
         uint32_t h[4];
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            h[j] = pack_half(__uint_as_float(u[j] << 16) * sc, __uint_as_float(u[j] & 0xffff0000u) * sc);
+            h[j] = pack_half(__uint_as_float(w[i][j] << 16) * sc, __uint_as_float(w[i][j] & 0xffff0000u) * sc);
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(tile + i * 16), "r"(h[0]), "r"(h[1]),
                      "r"(h[2]), "r"(h[3])
                      : "memory");
@@ -204,13 +221,14 @@ __device__ __forceinline__ void fill_image(unsigned char *image, const float (&q
 
 // ADJ: the adjoint's images as well as the forward's.
 template <int DK, bool ADJ>
-__global__ void __launch_bounds__(kPrepWarps * 32, 1) gdr_prep_kernel(PrepArgs a) {
+__global__ void __launch_bounds__(prep_warps<ADJ>() * 32, 1) gdr_prep_kernel(PrepArgs a) {
     using KI = KeyImage<DK>;
     extern __shared__ __align__(128) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned char *keys = smem + warp * prep_warp_bytes<DK, ADJ>();
     unsigned char *fwd = keys + KI::BYTES, *adj = fwd + forward_bytes<ADJ>();
-    float *scratch = reinterpret_cast<float *>(adj + (ADJ ? HeadImage<true>::BYTES : 0));
+    // where P will stand: the adjoint's, where there is one (the forward's image then ends before P)
+    float *scratch = reinterpret_cast<float *>(ADJ ? adj + HeadImage<true>::P : fwd + HeadImage<false>::P);
     const uint32_t kt = smem_u32(keys) + KI::K, qt = smem_u32(keys) + KI::Q;
 
     const int split = blockIdx.x % a.splits, pair = blockIdx.x / a.splits;
@@ -218,15 +236,19 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 1) gdr_prep_kernel(PrepArgs a
     const Span span = sequence_span(a.cu, n, a.T);
     const int chunks = (span.len + kChunk - 1) / kChunk;
     const int r0 = lane >> 2, c0 = 2 * (lane & 3);
-
-    for (int c = split * kPrepWarps + warp; c < chunks; c += a.splits * kPrepWarps) {
+    for (int c = split * prep_warps<ADJ>() + warp; c < chunks; c += a.splits * prep_warps<ADJ>()) {
         const int valid = min(kChunk, span.len - c * kChunk);
         const int64_t row = span.row + (int64_t)c * kChunk + lane, slot = first_chunk(span, n) + c;
         const bool live = lane < valid;
         if (lane == 0) bulk_store_wait_read();   // the images before have left shared memory
         __syncwarp();
-        const float ik = scale_row<DK>(a.k + (row * a.Hk + hk) * DK, kt, KI::KP, live);
-        const float iq = scale_row<DK>(a.q + (row * a.Hk + hk) * DK, qt, KI::KP, live);
+        const int64_t koff = ((row - lane) * a.Hk + hk) * DK, stride = (int64_t)a.Hk * DK;
+        copy_rows<DK>(kt, KI::KP, a.k + koff, stride, valid);
+        copy_rows<DK>(qt, KI::KP, a.q + koff, stride, valid);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        const float ik = scale_row<DK>(kt, KI::KP);
+        const float iq = scale_row<DK>(qt, KI::KP);
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
@@ -313,14 +335,49 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 1) gdr_prep_kernel(PrepArgs a
     if (lane == 0) bulk_store_wait();
 }
 
+// The sequences from the longest to the shortest, ties by index, so that the longest chains start
+// first.  One CTA; beyond kOrderMost sequences their order is kept.
+constexpr int kOrderMost = 4096;
+__global__ void __launch_bounds__(1024) gdr_order_kernel(const int32_t *cu, int64_t T, int N, int32_t *order) {
+    __shared__ int len[kOrderMost];
+    if (N > kOrderMost) {
+        for (int i = threadIdx.x; i < N; i += blockDim.x) order[i] = i;
+        return;
+    }
+    // offsets clamped and raised to the largest before them, 32 sequences at a time
+    if (threadIdx.x < 32) {
+        int top = 0;
+        for (int i0 = 0; i0 <= N; i0 += 32) {
+            const int i = i0 + threadIdx.x;
+            const int64_t c = i <= N ? cu[i] : 0;
+            int x = max(top, (int)(c < 0 ? 0 : (c > T ? T : c)));
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, x, m);
+                if ((int)threadIdx.x >= m) x = max(x, o);
+            }
+            const int before = __shfl_up_sync(0xffffffffu, x, 1);
+            if (i >= 1 && i <= N) len[i - 1] = x - (threadIdx.x == 0 ? top : before);
+            top = __shfl_sync(0xffffffffu, x, 31);
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < N; i += blockDim.x) {
+        const int mine = len[i];
+        int place = 0;
+        for (int j = 0; j < N; ++j) place += len[j] > mine || (len[j] == mine && j < i);
+        order[place] = i;
+    }
+}
+
 template <int DK, bool ADJ>
 static cudaError_t launch_prep_t(const PrepArgs &a, int64_t pairs, cudaStream_t st) {
-    constexpr int bytes = kPrepWarps * prep_warp_bytes<DK, ADJ>();
+    constexpr int bytes = prep_warps<ADJ>() * prep_warp_bytes<DK, ADJ>();
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     const auto kernel = gdr_prep_kernel<DK, ADJ>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(pairs * a.splits), kPrepWarps * 32, bytes, st>>>(a);
+    kernel<<<(unsigned)(pairs * a.splits), prep_warps<ADJ>() * 32, bytes, st>>>(a);
     e = cudaGetLastError();
     Profiler::mark(st);
     return e;
@@ -333,17 +390,19 @@ static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 size_t gdr_image_bytes(int64_t rows, int N, int Hk, int H, int dk, bool adjoint) {
     const size_t slots = (size_t)gdr::chunk_slots(rows, N);
     const size_t key = dk == 64 ? gdr::KeyImage<64>::BYTES : gdr::KeyImage<128>::BYTES;
-    return up256(slots * Hk * key) + up256(slots * H * gdr::HeadImage<false>::BYTES) +
+    return up256(slots * Hk * key) + up256(slots * H * gdr::HeadImage<false>::BYTES) + up256((size_t)N * 4) +
            (adjoint ? up256(slots * H * gdr::HeadImage<true>::BYTES) : 0);
 }
 
-GdrImages gdr_images(void *space, int64_t rows, int N, int Hk, int H, int dk, bool adjoint) {
-    const size_t slots = (size_t)gdr::chunk_slots(rows, N);
-    const size_t key = dk == 64 ? gdr::KeyImage<64>::BYTES : gdr::KeyImage<128>::BYTES;
+GdrImages gdr_images(void *space, const GdrArgs &a, bool adjoint) {
+    const size_t slots = (size_t)gdr::chunk_slots(a.rows, a.N);
+    const size_t key = a.dk == 64 ? gdr::KeyImage<64>::BYTES : gdr::KeyImage<128>::BYTES;
     GdrImages m;
     m.keys = static_cast<unsigned char *>(space);
-    m.forward = m.keys + up256(slots * Hk * key);
-    m.adjoint = adjoint ? m.forward + up256(slots * H * gdr::HeadImage<false>::BYTES) : nullptr;
+    m.forward = m.keys + up256(slots * a.Hk * key);
+    unsigned char *order = m.forward + up256(slots * a.H * gdr::HeadImage<false>::BYTES);
+    m.order = a.cu_seqlens && a.N > 1 ? reinterpret_cast<int32_t *>(order) : nullptr;
+    m.adjoint = adjoint ? order + up256((size_t)a.N * 4) : nullptr;
     return m;
 }
 
@@ -352,10 +411,16 @@ cudaError_t launch_gdr_prep(const GdrArgs &p, const GdrImages &m, cudaStream_t s
     const int64_t pairs = (int64_t)p.N * p.Hk;
     // CTAs per (sequence, key head): enough for a few rounds over the SMs, at most one per six chunks of
     // the longest sequence there can be
-    const int64_t most = (p.T + gdr::kPrepWarps * gdr::kChunk - 1) / (gdr::kPrepWarps * gdr::kChunk);
+    const int64_t most = (p.T + 6 * gdr::kChunk - 1) / (6 * gdr::kChunk);
     int64_t splits = (148 * 8 + pairs - 1) / pairs;
     splits = splits < most ? splits : most;
     if (splits < 1) splits = 1;
+    if (m.order) {
+        gdr::gdr_order_kernel<<<1, 1024, 0, st>>>(p.cu_seqlens, p.T, p.N, m.order);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        Profiler::mark(st);
+    }
     gdr::PrepArgs a{(const bf *)p.q, (const bf *)p.k, (const bf *)p.g, (const bf *)p.beta, p.cu_seqlens,
                     p.T, p.Hk, p.H, (int)splits, m.keys, m.forward, m.adjoint};
     if (m.adjoint)
