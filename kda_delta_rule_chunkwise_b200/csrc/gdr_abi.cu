@@ -79,7 +79,7 @@ kda_status kda_gdr_chunk_prefill(const void *q, const void *k, const void *v, co
     }
     const kda::GdrTokenArgs a{q, k, v, g, beta, state_in, state_out, cu_seqlens, nullptr,
                               nullptr, T, N, N, Hk, H, dk, dv, o, err};
-    return from_cuda(kda::launch_gdr_token(a, false, st));
+    return from_cuda(kda::launch_gdr_token_prefill(a, st));
 }
 
 kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const void *g,

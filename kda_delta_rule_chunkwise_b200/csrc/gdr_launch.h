@@ -65,6 +65,7 @@ struct GdrTokenArgs {
     void *o;
     uint32_t *err;
 };
-cudaError_t launch_gdr_token(const GdrTokenArgs &a, bool bf16, cudaStream_t st);
+cudaError_t launch_gdr_token(const GdrTokenArgs &a, bool bf16, cudaStream_t st);   // no cu_seqlens
+cudaError_t launch_gdr_token_prefill(const GdrTokenArgs &a, cudaStream_t st);      // fp32; no slots, lens
 
 }  // namespace kda

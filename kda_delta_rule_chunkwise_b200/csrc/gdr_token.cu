@@ -1,5 +1,5 @@
 // Gated delta rule, token by token in fp32: the decode step (one or a few tokens per
-// request, either input type) and the prefill of fp32 inputs.
+// request, either input type) and, by a kernel of its own below, the prefill of fp32 inputs.
 //
 // Per (request n, value head h) and token, with a = exp(g):
 //     p = S^T k;  y = S^T q;  delta = beta (v - a p);  o = a y + (k.q) delta
@@ -31,8 +31,8 @@ __global__ void __launch_bounds__(256) gdr_token_kernel(GdrTokenArgs a) {
     const int slice = blockIdx.x % slices, unit = blockIdx.x / slices;
     const int h = unit % a.H, n = unit / a.H, hk = h / (a.H / a.Hk);
 
-    const Span span = sequence_span(a.cu_seqlens, n, a.T);
-    int len = span.len;
+    const int64_t first = (int64_t)n * a.T;   // row of the request's first token
+    int len = (int)a.T;
     if (a.lens) len = min(max(a.lens[n], 0), len);
     int64_t entry = n;
     if (a.slots) {
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(256) gdr_token_kernel(GdrTokenArgs a) {
     const Tin *q = (const Tin *)a.q, *k = (const Tin *)a.k, *v = (const Tin *)a.v;
     float in_k = 0.f, in_v = 0.f, in_g = 0.f;
     auto fetch = [&](int t) {
-        const int64_t row = span.row + t;
+        const int64_t row = first + t;
         if (tid < DK) in_k = to_f32(k[(row * a.Hk + hk) * DK + tid]);
         else if (tid >= 128 && tid < 128 + DK) in_k = to_f32(q[(row * a.Hk + hk) * DK + tid - 128]);
         if (tid < DVS) in_v = to_f32(v[(row * a.H + h) * a.dv + slice * DVS + tid]);
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256) gdr_token_kernel(GdrTokenArgs a) {
             }
             const float d = gb[b][1] * (vs[b][tid] - dec * pj);
             dl[b][tid] = d;
-            ((Tin *)a.o)[((span.row + t) * a.H + h) * a.dv + slice * DVS + tid] =
+            ((Tin *)a.o)[((first + t) * a.H + h) * a.dv + slice * DVS + tid] =
                 from_f32<Tin>(fmaf(kq[b], d, dec * yj));
         }
         __syncthreads();
@@ -141,6 +141,118 @@ __global__ void __launch_bounds__(256) gdr_token_kernel(GdrTokenArgs a) {
             __stcs(reinterpret_cast<float4 *>(a.state_out + soff + (int64_t)(rg + i * RG) * a.dv) + cg,
                    s[i]);
     }
+}
+
+// Prefill of fp32 inputs.  The same step, with nothing between the tokens but one warp: it keeps
+// four columns of a state, each lane the rows lane + 32 i, and takes the eight sums over channels
+// (S^T k and S^T q) in one halving exchange of nine shuffles.  No barrier and no shared memory;
+// the inputs of the next four tokens are loaded while four are worked on.  What bounds it is the
+// latency of a token's dependent steps, about 250 cycles, so many narrow warps run side by side.
+template <int DK>
+__global__ void __launch_bounds__(128) gdr_token_prefill_kernel(GdrTokenArgs a) {
+    constexpr int R = DK / 32, AHEAD = 4;
+    const int lane = threadIdx.x & 31, groups = a.dv / 4;
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (w >= (int64_t)a.N * a.H * groups) return;
+    const int cg = (int)(w % groups), unit = (int)(w / groups);
+    const int h = unit % a.H, n = unit / a.H, hk = h / (a.H / a.Hk);
+    const Span span = sequence_span(a.cu_seqlens, n, a.T);
+    const int64_t soff = ((int64_t)n * a.H + h) * DK * a.dv + cg * 4;
+    const int mine = (lane >> 2) & 3;   // the column whose sums this lane ends up with
+
+    float4 s[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        s[i] = a.state_in ? *reinterpret_cast<const float4 *>(a.state_in + soff + (int64_t)(lane + 32 * i) * a.dv)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float *q = (const float *)a.q + (span.row * a.Hk + hk) * DK + lane;
+    const float *k = (const float *)a.k + (span.row * a.Hk + hk) * DK + lane;
+    const float *v = (const float *)a.v + (span.row * a.H + h) * a.dv + cg * 4 + mine;
+    const float *g = (const float *)a.g + span.row * a.H + h, *beta = (const float *)a.beta + span.row * a.H + h;
+    float *o = (float *)a.o + (span.row * a.H + h) * a.dv + cg * 4 + mine;
+    const int64_t kstride = (int64_t)a.Hk * DK, vstride = (int64_t)a.H * a.dv;
+
+    struct Token {
+        float k[R], q[R], v, g, b;
+    };
+    auto fetch = [&](Token (&t)[AHEAD], int from) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int64_t at = from + j;
+            const bool live = at < span.len;   // a token of zeros changes nothing
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                t[j].k[i] = live ? __ldg(k + at * kstride + 32 * i) : 0.f;
+                t[j].q[i] = live ? __ldg(q + at * kstride + 32 * i) : 0.f;
+            }
+            t[j].v = live ? __ldg(v + at * vstride) : 0.f;
+            t[j].g = live ? __ldg(g + at * a.H) : 0.f;
+            t[j].b = live ? __ldg(beta + at * a.H) : 0.f;
+        }
+    };
+    Token now[AHEAD], next[AHEAD];
+    fetch(next, 0);
+    for (int t0 = 0; t0 < span.len; t0 += AHEAD) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) now[j] = next[j];
+        fetch(next, t0 + AHEAD);
+        float kq[AHEAD], dec[AHEAD];   // k.q and the decays do not wait for the state
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < R; ++i) x = fmaf(now[j].k[i], now[j].q[i], x);
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+            kq[j] = x;
+            dec[j] = expf(fmaxf(now[j].g, kMinLogDecay));
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            // sums 0-3: S^T k of the four columns, 4-7: S^T q
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float kr = now[j].k[i], qr = now[j].q[i];
+                x[0] = fmaf(s[i].x, kr, x[0]); x[1] = fmaf(s[i].y, kr, x[1]);
+                x[2] = fmaf(s[i].z, kr, x[2]); x[3] = fmaf(s[i].w, kr, x[3]);
+                x[4] = fmaf(s[i].x, qr, x[4]); x[5] = fmaf(s[i].y, qr, x[5]);
+                x[6] = fmaf(s[i].z, qr, x[6]); x[7] = fmaf(s[i].w, qr, x[7]);
+            }
+            // each step halves the sums a lane has: bit 4 of the lane picks k or q, bits 3 and 2 the column
+#pragma unroll
+            for (int half = 4; half > 0; half >>= 1) {
+                const int m = half * 4;
+                const bool up = (lane & m) != 0;
+#pragma unroll
+                for (int i = 0; i < half; ++i) {
+                    const float give = up ? x[i] : x[i + half], keep = up ? x[i + half] : x[i];
+                    x[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+                }
+            }
+            float z = x[0];
+            z += __shfl_xor_sync(0xffffffffu, z, 2);
+            z += __shfl_xor_sync(0xffffffffu, z, 1);
+            // lanes with bit 4 clear hold S^T k, the others S^T q
+            const float d = now[j].b * (now[j].v - dec[j] * z);
+            const float d0 = __shfl_sync(0xffffffffu, d, 0), d1 = __shfl_sync(0xffffffffu, d, 4);
+            const float d2 = __shfl_sync(0xffffffffu, d, 8), d3 = __shfl_sync(0xffffffffu, d, 12);
+            const float dm = mine & 2 ? (mine & 1 ? d3 : d2) : (mine & 1 ? d1 : d0);
+            if ((lane & 19) == 16 && t0 + j < span.len) o[(t0 + j) * vstride] = fmaf(kq[j], dm, dec[j] * z);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float kr = now[j].k[i];
+                s[i].x = fmaf(kr, d0, dec[j] * s[i].x); s[i].y = fmaf(kr, d1, dec[j] * s[i].y);
+                s[i].z = fmaf(kr, d2, dec[j] * s[i].z); s[i].w = fmaf(kr, d3, dec[j] * s[i].w);
+            }
+        }
+    }
+    if (a.state_out)
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            *reinterpret_cast<float4 *>(a.state_out + soff + (int64_t)(lane + 32 * i) * a.dv) = s[i];
 }
 
 template <int DK, int DVS, typename Tin>
@@ -168,6 +280,16 @@ cudaError_t launch_gdr_token(const GdrTokenArgs &a, bool bf16, cudaStream_t st) 
                     : gdr::launch_token_d<64, float>(a, st);
     return bf16 ? gdr::launch_token_d<128, __nv_bfloat16>(a, st)
                 : gdr::launch_token_d<128, float>(a, st);
+}
+
+cudaError_t launch_gdr_token_prefill(const GdrTokenArgs &a, cudaStream_t st) {
+    const int64_t warps = (int64_t)a.N * a.H * (a.dv / 4);
+    const unsigned grid = (unsigned)((warps + 3) / 4);
+    if (a.dk == 64) gdr::gdr_token_prefill_kernel<64><<<grid, 128, 0, st>>>(a);
+    else gdr::gdr_token_prefill_kernel<128><<<grid, 128, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    Profiler::mark(st);
+    return e;
 }
 
 }  // namespace kda
