@@ -364,6 +364,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32)
 
 // ---------------------------------------------------------------- gradients of a block
 constexpr int kBlock = 64;
+constexpr int kGradWarps = 16, kGradThreads = kGradWarps * 32;
 
 struct GradsArgs {
     const __nv_bfloat16 *q, *k, *dout, *g, *beta;
@@ -383,10 +384,10 @@ struct GradsSmem {
     static constexpr int DP = Z + DK * VP, DA = DP + kBlock * MP;
     static constexpr int F = DA + kBlock * MP;   // floats from here
     // per-row values and partial sums
-    enum { GH = 0, GL = 1, INTO = 2, OUT = 3, BETA = 4, DBETA = 5, ROW = 6 /* 2 */, STATE = 8 /* 2 */,
-           WRITE = 10 /* 2 */, COL = 12 /* 4 */, COUNT = 16 };
+    enum { GH = 0, GL = 1, INTO = 2, OUT = 3, BETA = 4, DBETA = 5, ROW = 6 /* 4 */, STATE = 10 /* 4 */,
+           WRITE = 14 /* 4 */, COL = 18 /* 4 */, COUNT = 22 };
     static constexpr int RED = F + COUNT * kBlock * 4;
-    static constexpr int BYTES = RED + 64 * 4;
+    static constexpr int BYTES = RED + 6 * kGradWarps * 4;
 };
 
 // A power of two that brings m (a tile's largest value) into [2^7, 2^8), and its inverse: a
@@ -458,12 +459,12 @@ __device__ __forceinline__ void product_add(float (&c)[NT][4], float f, uint32_t
 }
 
 // One CTA per (64-token block, key head); it walks the value heads of the key head's group and
-// sums dq and dk over them in registers, in order.  Warp w has rows 16 (w % 4) .. and the half
+// sums dq and dk over them in registers, in order.  Warp w has rows 16 (w % 4) .. and the quarter
 // w / 4 of the columns.
 template <int DK, int DV>
-__global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
+__global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a) {
     using M = GradsSmem<DK, DV>;
-    constexpr int NF = DK / 16;   // column tiles of a warp in [64][DK] results
+    constexpr int NF = DK / 32;   // column tiles of a warp in [64][DK] results
     extern __shared__ __align__(128) unsigned char smem[];
     float *rows = reinterpret_cast<float *>(smem + M::F);
     float *red = reinterpret_cast<float *>(smem + M::RED);
@@ -484,21 +485,21 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
     auto cta_max = [&](float m, int at) {
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-        if (lane == 0) red[at * 8 + warp] = m;
+        if (lane == 0) red[at * kGradWarps + warp] = m;
         __syncthreads();
-        m = red[at * 8];
+        m = red[at * kGradWarps];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) m = fmaxf(m, red[at * 8 + w]);
+        for (int w = 1; w < kGradWarps; ++w) m = fmaxf(m, red[at * kGradWarps + w]);
         return m;
     };
     // a [64][D] bf16 tile, row r at src + r stride: scaled fp16 into shared memory
     auto load_bf16 = [&](auto dconst, const __nv_bfloat16 *src, int64_t stride, int dst, int pitch, int at) {
-        constexpr int D = decltype(dconst)::value, PER = kBlock * D / 8 / 256;
+        constexpr int D = decltype(dconst)::value, PER = kBlock * D / 8 / kGradThreads;
         uint4 w[PER];
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int x = i * 256 + tid, r = x / (D / 8), c = x % (D / 8);
+            const int x = i * kGradThreads + tid, r = x / (D / 8), c = x % (D / 8);
             w[i] = make_uint4(0u, 0u, 0u, 0u);
             if (r < valid) w[i] = __ldg(reinterpret_cast<const uint4 *>(src + r * stride) + c);
             for (uint32_t u : {w[i].x, w[i].y, w[i].z, w[i].w})
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
         const float f = tile_scale(cta_max(m, at), inv);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int x = i * 256 + tid, r = x / (D / 8), c = x % (D / 8);
+            const int x = i * kGradThreads + tid, r = x / (D / 8), c = x % (D / 8);
             *reinterpret_cast<uint4 *>(smem + dst + r * pitch + c * 16) =
                 make_uint4(pack_half(bf_lo(w[i].x) * f, bf_hi(w[i].x) * f),
                            pack_half(bf_lo(w[i].y) * f, bf_hi(w[i].y) * f),
@@ -518,12 +519,12 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
         return inv;
     };
     auto load_f32 = [&](const float *src, int64_t stride, int dst, int at) {
-        constexpr int PER = kBlock * DV / 4 / 256;
+        constexpr int PER = kBlock * DV / 4 / kGradThreads;
         float4 w[PER];
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int x = i * 256 + tid, r = x / (DV / 4), c = x % (DV / 4);
+            const int x = i * kGradThreads + tid, r = x / (DV / 4), c = x % (DV / 4);
             w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < valid) w[i] = __ldcs(reinterpret_cast<const float4 *>(src + r * stride) + c);
             m = fmaxf(m, fmaxf(fmaxf(fabsf(w[i].x), fabsf(w[i].y)), fmaxf(fabsf(w[i].z), fabsf(w[i].w))));
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
         const float f = tile_scale(cta_max(m, at), inv);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int x = i * 256 + tid, r = x / (DV / 4), c = x % (DV / 4);
+            const int x = i * kGradThreads + tid, r = x / (DV / 4), c = x % (DV / 4);
             *reinterpret_cast<uint2 *>(smem + dst + r * M::VP + c * 8) =
                 make_uint2(pack_half(w[i].x * f, w[i].y * f), pack_half(w[i].z * f, w[i].w * f));
         }
@@ -545,10 +546,10 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
     const float sk = load_bf16(DKc{}, a.k + koff, kstride, M::K, M::KP, 0);
     const float sq = load_bf16(DKc{}, a.q + koff, kstride, M::Q, M::KP, 1);
     __syncthreads();
-    // Q K^T and K K^T, columns 32 wn ..
-    float qk[4][4], kk[4][4];
-    product_nt<4, DK / 16>(qk, sb + M::Q + wm * 16 * M::KP, M::KP, sb + M::K + wn * 32 * M::KP, M::KP);
-    product_nt<4, DK / 16>(kk, sb + M::K + wm * 16 * M::KP, M::KP, sb + M::K + wn * 32 * M::KP, M::KP);
+    // Q K^T and K K^T, columns 16 wn ..
+    float qk[2][4], kk[2][4];
+    product_nt<2, DK / 16>(qk, sb + M::Q + wm * 16 * M::KP, M::KP, sb + M::K + wn * 16 * M::KP, M::KP);
+    product_nt<2, DK / 16>(kk, sb + M::K + wm * 16 * M::KP, M::KP, sb + M::K + wn * 16 * M::KP, M::KP);
 
     float dq[NF][4], dk[NF][4];
 #pragma unroll
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
             const float4 *s4 = reinterpret_cast<const float4 *>(a.s_blocks + unit * DK * DV);
             const float4 *z4 = reinterpret_cast<const float4 *>(a.z_blocks + unit * DK * DV);
 #pragma unroll 8
-            for (int x = tid; x < DK * DV / 4; x += 256) {
+            for (int x = tid; x < DK * DV / 4; x += kGradThreads) {
                 const float4 u = __ldcs(s4 + x), v = __ldcs(z4 + x);
                 dot += u.x * v.x + u.y * v.y + (u.z * v.z + u.w * v.w);
                 const int c = x / (DV / 4), j = x % (DV / 4);
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
             }
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
-            if (lane == 0) red[40 + warp] = dot;
+            if (lane == 0) red[5 * kGradWarps + warp] = dot;
         }
         __syncthreads();
 
@@ -634,19 +635,19 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
         // fp16 copies of dP and dA in units of the operands' scales, at most 2^15 for beta <= 4
         constexpr float kDown = 1.f / 4096.f;
         {
-            float m1[4][4], m2[4][4], sum[2] = {0.f, 0.f}, col[4][2];
-            product_nt<4, DV / 16>(m1, sb + M::DO + wm * 16 * M::VP, M::VP, sb + M::NN + wn * 32 * M::VP, M::VP);
-            product_nt<4, DV / 16>(m2, sb + M::E + wm * 16 * M::VP, M::VP, sb + M::NN + wn * 32 * M::VP, M::VP);
+            float m1[2][4], m2[2][4], sum[2] = {0.f, 0.f}, col[2][2];
+            product_nt<2, DV / 16>(m1, sb + M::DO + wm * 16 * M::VP, M::VP, sb + M::NN + wn * 16 * M::VP, M::VP);
+            product_nt<2, DV / 16>(m2, sb + M::E + wm * 16 * M::VP, M::VP, sb + M::NN + wn * 16 * M::VP, M::VP);
             const float w1 = so * sn * (sq * sk), w2 = se * sn * (sk * sk);
             const float gha = rows[M::GH * kBlock + ra], gla = rows[M::GL * kBlock + ra];
             const float ghb = rows[M::GH * kBlock + rb], glb = rows[M::GL * kBlock + rb];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < 2; ++t) {
                 float p[4], d[4];
                 col[t][0] = col[t][1] = 0.f;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const int s = wn * 32 + t * 8 + cc + (x & 1), r = x < 2 ? ra : rb;
+                    const int s = wn * 16 + t * 8 + cc + (x & 1), r = x < 2 ? ra : rb;
                     const float hs = rows[M::GH * kBlock + s], ls = rows[M::GL * kBlock + s];
                     const float bs = rows[M::BETA * kBlock + s];
                     const float D = s <= r ? exp2_approx(((x < 2 ? gha : ghb) - hs) + ((x < 2 ? gla : glb) - ls)) : 0.f;
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
                 }
 #pragma unroll
                 for (int x = 0; x < 4; x += 2) {
-                    const int at = (x ? rb : ra) * M::MP + (wn * 32 + t * 8 + cc) * 2;
+                    const int at = (x ? rb : ra) * M::MP + (wn * 16 + t * 8 + cc) * 2;
                     *reinterpret_cast<uint32_t *>(smem + M::DP + at) = pack_half(p[x] * kDown, p[x + 1] * kDown);
                     *reinterpret_cast<uint32_t *>(smem + M::DA + at) = pack_half(d[x] * kDown, d[x + 1] * kDown);
                 }
@@ -671,12 +672,12 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
                 if ((lane & 3) == 0) rows[(M::ROW + wn) * kBlock + (i ? rb : ra)] = sum[i];
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
 #pragma unroll
                     for (int m = 4; m < 32; m <<= 1) col[t][x] += __shfl_xor_sync(0xffffffffu, col[t][x], m);
-                    if (lane < 4) rows[(M::COL + wm) * kBlock + wn * 32 + t * 8 + cc + x] = col[t][x];
+                    if (lane < 4) rows[(M::COL + wm) * kBlock + wn * 16 + t * 8 + cc + x] = col[t][x];
                 }
         }
         // the state's share: rows of dO S^T, E S^T and N Z^T, columns 8 NF wn ..
@@ -743,11 +744,11 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float *p = rows + 2 * lane + i;
-                from[i] = p[M::ROW * kBlock] + p[(M::ROW + 1) * kBlock] -
-                          (p[M::COL * kBlock] + p[(M::COL + 1) * kBlock] +
-                           (p[(M::COL + 2) * kBlock] + p[(M::COL + 3) * kBlock])) +
-                          (p[M::STATE * kBlock] + p[(M::STATE + 1) * kBlock]);
-                w[i] = p[M::WRITE * kBlock] + p[(M::WRITE + 1) * kBlock];
+                auto four = [&](int at) {
+                    return (p[at * kBlock] + p[(at + 1) * kBlock]) + (p[(at + 2) * kBlock] + p[(at + 3) * kBlock]);
+                };
+                from[i] = four(M::ROW) - four(M::COL) + four(M::STATE);
+                w[i] = four(M::WRITE);
             }
             float suf = from[0] + from[1], pre = w[0] + w[1];
 #pragma unroll
@@ -758,7 +759,7 @@ __global__ void __launch_bounds__(256, 1) gdr_grads_kernel(GradsArgs a) {
             }
             float d = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d += red[40 + i];
+            for (int i = 0; i < kGradWarps; ++i) d += red[5 * kGradWarps + i];
             d *= rows[M::INTO * kBlock + kBlock - 1];
             const float before = pre - w[0] - w[1];
             const float dg[2] = {suf + before + d, suf - from[0] + before + w[0] + d};
@@ -809,7 +810,7 @@ static cudaError_t launch_grads_t(const GradsArgs &a, int64_t blocks, cudaStream
     cudaError_t e = cudaFuncSetAttribute(gdr_grads_kernel<DK, DV>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    gdr_grads_kernel<DK, DV><<<(unsigned)(blocks * a.Hk), 256, bytes, st>>>(a);
+    gdr_grads_kernel<DK, DV><<<(unsigned)(blocks * a.Hk), kGradThreads, bytes, st>>>(a);
     e = cudaGetLastError();
     Profiler::mark(st);
     return e;
