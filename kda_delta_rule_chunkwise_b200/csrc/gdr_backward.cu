@@ -70,14 +70,18 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32)
     const int j0 = slice * W + group * 16, jr = lane >> 2, tc = 2 * (lane & 3);
     const int c0 = part * (DK / KS);
     float z[NC][4];   // Z^T, laid out like the forward's S^T
+    float zm0 = 0.f, zm1 = 0.f;   // this lane's largest |Z| of its two columns
     const int64_t state_off = ((int64_t)n * a.H + h) * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
     {
         const float *in = args.dstate_out ? args.dstate_out + state_off : nullptr;
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < NC; ++i) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 z[i][x] = in ? in[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] : 0.f;
+            zm0 = fmaxf(zm0, fmaxf(fabsf(z[i][0]), fabsf(z[i][1])));
+            zm1 = fmaxf(zm1, fmaxf(fabsf(z[i][2]), fabsf(z[i][3])));
+        }
     }
     const int nrow = (lane & 7) + (lane >> 4) * 8, ncol = ((lane >> 3) & 1) * 16;
     const int trow = lane & 15, tcol = (lane >> 4) * 16;
@@ -121,15 +125,9 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32)
                 for (int x = 0; x < 4; ++x)
                     dst[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] = z[i][x];
         }
-        float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            m0 = fmaxf(m0, fmaxf(fabsf(z[i][0]), fabsf(z[i][1])));
-            m1 = fmaxf(m1, fmaxf(fabsf(z[i][2]), fabsf(z[i][3])));
-        }
-        float iz0, iz1;
-        const float fz0 = row_scale(quad_max(m0), iz0), fz1 = row_scale(quad_max(m1), iz1);
-        if (block_end) store_top(args.tops + (blk * (a.dv / 16) + j0 / 16) * 2, fmaxf(m0, m1), KS, part);
+        float m0, m1, iz0, iz1;
+        const float fz0 = row_scale(quad_max(zm0), iz0), fz1 = row_scale(quad_max(zm1), iz1);
+        if (block_end) store_top(args.tops + (blk * (a.dv / 16) + j0 / 16) * 2, fmaxf(zm0, zm1), KS, part);
 
         ok = pipe.wait(pipe.full + st, (it / M::ST) & 1);
         if (!ok) break;
@@ -165,48 +163,41 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32)
         if (KS == 2) {
             float4 *mine = reinterpret_cast<float4 *>(smem + M::SWAP) +
                            (((group * 2 + (it & 1)) * 2 + part) * XF / 4) * 32 + lane;
-            const float4 *other = mine + (part ? -1 : 1) * (XF / 4) * 32;
 #pragma unroll
             for (int t = 0; t < 4; ++t) mine[t * 32] = make_float4(y[t][0], y[t][1], y[t][2], y[t][3]);
             __syncwarp();
             if (lane == 0) mbar_arrive(pipe.swapped + group * 2 + (part ^ 1));
             if (it > 0) write_dv(row + kChunk, valid - kChunk);   // the chunk after this one
-            ok = pipe.wait(pipe.swapped + group * 2 + part, it & 1);
-            if (!ok) break;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const float4 o = other[t * 32];
-                y[t][0] += o.x; y[t][1] += o.y; y[t][2] += o.z; y[t][3] += o.w;
-            }
         }
-        // dO^T in the scaled units of Q' (exact: powers of two)
-        float o[4][4];
-        m0 = m1 = 0.f;
-#pragma unroll
-        for (int t = 0; t < 4; t += 2) {
-            uint32_t v[4];
-            ldsm4_t(v, sb + L::v_at(8 * t + nrow, group * 2 + ((lane >> 3) & 1)));
-            if (valid < kChunk) clear_rows(v, 8 * t + tc, valid);   // the rows behind the sequence's end
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float2 iq = *reinterpret_cast<const float2 *>(scal + L::IQ * kChunk + 8 * (t + u) + tc);
-                o[t + u][0] = __uint_as_float(v[2 * u] << 16) * iq.x;
-                o[t + u][1] = __uint_as_float(v[2 * u] & 0xffff0000u) * iq.y;
-                o[t + u][2] = __uint_as_float(v[2 * u + 1] << 16) * iq.x;
-                o[t + u][3] = __uint_as_float(v[2 * u + 1] & 0xffff0000u) * iq.y;
-                m0 = fmaxf(m0, fmaxf(fabsf(o[t + u][0]), fabsf(o[t + u][1])));
-                m1 = fmaxf(m1, fmaxf(fabsf(o[t + u][2]), fabsf(o[t + u][3])));
-            }
-        }
-        // dU = ik (P'^T dO + exp(G_C - G) K Z): token r of P as the contraction
-        float e[4][4];
+        // What does not depend on the other half, while its sums are on their way: dO^T in the scaled
+        // units of Q' (exact: powers of two), P'^T dO, and Z <- Gamma_C Z + (Gamma dO)^T Q'.
+        float pu[4][4];
         {
-            float io0, io1, pu[4][4];
+            float o[4][4];
+            m0 = m1 = 0.f;
+#pragma unroll
+            for (int t = 0; t < 4; t += 2) {
+                uint32_t v[4];
+                ldsm4_t(v, sb + L::v_at(8 * t + nrow, group * 2 + ((lane >> 3) & 1)));
+                if (valid < kChunk) clear_rows(v, 8 * t + tc, valid);   // the rows behind the sequence's end
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float2 iq = *reinterpret_cast<const float2 *>(scal + L::IQ * kChunk + 8 * (t + u) + tc);
+                    o[t + u][0] = __uint_as_float(v[2 * u] << 16) * iq.x;
+                    o[t + u][1] = __uint_as_float(v[2 * u] & 0xffff0000u) * iq.y;
+                    o[t + u][2] = __uint_as_float(v[2 * u + 1] << 16) * iq.x;
+                    o[t + u][3] = __uint_as_float(v[2 * u + 1] & 0xffff0000u) * iq.y;
+                    m0 = fmaxf(m0, fmaxf(fabsf(o[t + u][0]), fabsf(o[t + u][1])));
+                    m1 = fmaxf(m1, fmaxf(fabsf(o[t + u][2]), fabsf(o[t + u][3])));
+                }
+            }
+            float io0, io1;
             const float fo0 = row_scale(quad_max(m0), io0), fo1 = row_scale(quad_max(m1), io1);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) pu[t][x] = 0.f;
+            m0 = m1 = 0.f;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 const uint32_t u[4] = {
@@ -224,16 +215,85 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32)
                     mma16816(pu[2 * half], u, bl[0], bl[1]);
                     mma16816(pu[2 * half + 1], u, bl[2], bl[3]);
                 }
+#pragma unroll
+                for (int t = 2 * ks; t < 2 * ks + 2; ++t) {   // Gamma dO (iq is a power of two)
+                    const float2 cq = *reinterpret_cast<const float2 *>(scal + L::CQ * kChunk + 8 * t + tc);
+                    const float2 iq = *reinterpret_cast<const float2 *>(scal + L::IQ * kChunk + 8 * t + tc);
+                    const float gx = __fdividef(cq.x, iq.x), gy = __fdividef(cq.y, iq.y);
+                    o[t][0] *= gx; o[t][1] *= gy; o[t][2] *= gx; o[t][3] *= gy;
+                    m0 = fmaxf(m0, fmaxf(fabsf(o[t][0]), fabsf(o[t][1])));
+                    m1 = fmaxf(m1, fmaxf(fabsf(o[t][2]), fabsf(o[t][3])));
+                }
             }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                pu[t][0] *= io0; pu[t][1] *= io0; pu[t][2] *= io1; pu[t][3] *= io1;
+            }
+            float iu0, iu1;
+            const float fu0 = row_scale(quad_max(m0), iu0), fu1 = row_scale(quad_max(m1), iu1);
+            const float gend = scal[L::MISC * kChunk];
+            uint32_t oh[2][4], ol[2][4];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int t = 2 * ks + (x >> 1), c = (x & 1) * 2;
+                    const float f = (x & 1) ? fu1 : fu0;
+                    split_half(o[t][c] * f, o[t][c + 1] * f, oh[ks][x], ol[ks][x]);
+                }
+#pragma unroll
+            for (int i = 0; i < NC; i += 4) {
+                float acc[4][4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) acc[t][x] = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    uint32_t b0[4], b1[4];
+                    ldsm4_t(b0, sb + L::Q + (16 * ks + trow) * L::KP + tcol + c0 * 2 + i * 16);
+                    ldsm4_t(b1, sb + L::Q + (16 * ks + trow) * L::KP + tcol + c0 * 2 + i * 16 + 32);
+                    mma16816(acc[0], oh[ks], b0[0], b0[1]);
+                    mma16816(acc[1], oh[ks], b0[2], b0[3]);
+                    mma16816(acc[2], oh[ks], b1[0], b1[1]);
+                    mma16816(acc[3], oh[ks], b1[2], b1[3]);
+                    mma16816(acc[0], ol[ks], b0[0], b0[1]);
+                    mma16816(acc[1], ol[ks], b0[2], b0[3]);
+                    mma16816(acc[2], ol[ks], b1[0], b1[1]);
+                    mma16816(acc[3], ol[ks], b1[2], b1[3]);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    z[i + t][0] = fmaf(gend, z[i + t][0], iu0 * acc[t][0]);
+                    z[i + t][1] = fmaf(gend, z[i + t][1], iu0 * acc[t][1]);
+                    z[i + t][2] = fmaf(gend, z[i + t][2], iu1 * acc[t][2]);
+                    z[i + t][3] = fmaf(gend, z[i + t][3], iu1 * acc[t][3]);
+                }
+            }
+        }
+        if (KS == 2) {
+            ok = pipe.wait(pipe.swapped + group * 2 + part, it & 1);
+            if (!ok) break;
+            const float4 *other = reinterpret_cast<const float4 *>(smem + M::SWAP) +
+                                  (((group * 2 + (it & 1)) * 2 + (part ^ 1)) * XF / 4) * 32 + lane;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const float4 x = other[t * 32];
+                y[t][0] += x.x; y[t][1] += x.y; y[t][2] += x.z; y[t][3] += x.w;
+            }
+        }
+        // dU = ik P'^T dO + exp(G_C - G) ik K' Z
+        float e[4][4];
+        {
             m0 = m1 = 0.f;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const float2 ik = *reinterpret_cast<const float2 *>(scal + L::IK * kChunk + 8 * t + tc);
-                const float2 ok = *reinterpret_cast<const float2 *>(scal + L::OK * kChunk + 8 * t + tc);
-                y[t][0] = ik.x * (io0 * pu[t][0]) + ok.x * y[t][0];
-                y[t][1] = ik.y * (io0 * pu[t][1]) + ok.y * y[t][1];
-                y[t][2] = ik.x * (io1 * pu[t][2]) + ok.x * y[t][2];
-                y[t][3] = ik.y * (io1 * pu[t][3]) + ok.y * y[t][3];
+                const float2 ok2 = *reinterpret_cast<const float2 *>(scal + L::OK * kChunk + 8 * t + tc);
+                y[t][0] = ik.x * pu[t][0] + ok2.x * y[t][0];
+                y[t][1] = ik.y * pu[t][1] + ok2.y * y[t][1];
+                y[t][2] = ik.x * pu[t][2] + ok2.x * y[t][2];
+                y[t][3] = ik.y * pu[t][3] + ok2.y * y[t][3];
                 m0 = fmaxf(m0, fmaxf(fabsf(y[t][0]), fabsf(y[t][1])));
                 m1 = fmaxf(m1, fmaxf(fabsf(y[t][2]), fabsf(y[t][3])));
             }
@@ -283,69 +343,66 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32)
                         dst[tok * vstride + (x >> 1) * 8] = e[t][x];
                 }
         }
-        // dV = dR = beta E; then Gamma dO and -Gamma dR in the scaled units of Q' and K'
+        // dV = dR = beta E; then Z -= (Gamma dR)^T K, in the scaled units of K'
         m0 = m1 = 0.f;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const float2 b = *reinterpret_cast<const float2 *>(scal + L::BETA * kChunk + 8 * t + tc);
             const float2 ck = *reinterpret_cast<const float2 *>(scal + L::CK * kChunk + 8 * t + tc);
-            const float2 cq = *reinterpret_cast<const float2 *>(scal + L::CQ * kChunk + 8 * t + tc);
-            const float2 iq = *reinterpret_cast<const float2 *>(scal + L::IQ * kChunk + 8 * t + tc);
-            const float gx = cq.x / iq.x, gy = cq.y / iq.y;   // Gamma (iq is a power of two)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 e[t][x] *= (x & 1) ? b.y : b.x;
-                o[t][x] *= (x & 1) ? gy : gx;
                 y[t][x] = -((x & 1) ? ck.y : ck.x) * e[t][x];
             }
             const __nv_bfloat162 w0 = __floats2bfloat162_rn(e[t][0], e[t][1]);
             const __nv_bfloat162 w1 = __floats2bfloat162_rn(e[t][2], e[t][3]);
             pk[t][0] = reinterpret_cast<const uint32_t &>(w0);
             pk[t][1] = reinterpret_cast<const uint32_t &>(w1);
-            m0 = fmaxf(m0, fmaxf(fmaxf(fabsf(y[t][0]), fabsf(y[t][1])), fmaxf(fabsf(o[t][0]), fabsf(o[t][1]))));
-            m1 = fmaxf(m1, fmaxf(fmaxf(fabsf(y[t][2]), fabsf(y[t][3])), fmaxf(fabsf(o[t][2]), fabsf(o[t][3]))));
+            m0 = fmaxf(m0, fmaxf(fabsf(y[t][0]), fabsf(y[t][1])));
+            m1 = fmaxf(m1, fmaxf(fabsf(y[t][2]), fabsf(y[t][3])));
         }
         {
             float iu0, iu1;
             const float fu0 = row_scale(quad_max(m0), iu0), fu1 = row_scale(quad_max(m1), iu1);
-            const float gend = scal[L::MISC * kChunk];
-            uint32_t oh[2][4], ol[2][4], rh[2][4], rl[2][4];
+            uint32_t rh[2][4], rl[2][4];
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int t = 2 * ks + (x >> 1), c = (x & 1) * 2;
                     const float f = (x & 1) ? fu1 : fu0;
-                    split_half(o[t][c] * f, o[t][c + 1] * f, oh[ks][x], ol[ks][x]);
                     split_half(y[t][c] * f, y[t][c + 1] * f, rh[ks][x], rl[ks][x]);
                 }
+            zm0 = zm1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < NC; i += 2) {
-                float acc[2][4], ac2[2][4];
+            for (int i = 0; i < NC; i += 4) {
+                float acc[4][4];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) acc[t][x] = ac2[t][x] = 0.f;
+                    for (int x = 0; x < 4; ++x) acc[t][x] = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
-                    uint32_t bq[4], bk[4];
-                    ldsm4_t(bq, sb + L::Q + (16 * ks + trow) * L::KP + tcol + c0 * 2 + i * 16);
-                    ldsm4_t(bk, sb + L::K + (16 * ks + trow) * L::KP + tcol + c0 * 2 + i * 16);
-                    mma16816(acc[0], oh[ks], bq[0], bq[1]);
-                    mma16816(acc[1], oh[ks], bq[2], bq[3]);
-                    mma16816(ac2[0], rh[ks], bk[0], bk[1]);
-                    mma16816(ac2[1], rh[ks], bk[2], bk[3]);
-                    mma16816(acc[0], ol[ks], bq[0], bq[1]);
-                    mma16816(acc[1], ol[ks], bq[2], bq[3]);
-                    mma16816(ac2[0], rl[ks], bk[0], bk[1]);
-                    mma16816(ac2[1], rl[ks], bk[2], bk[3]);
+                    uint32_t b0[4], b1[4];
+                    ldsm4_t(b0, sb + L::K + (16 * ks + trow) * L::KP + tcol + c0 * 2 + i * 16);
+                    ldsm4_t(b1, sb + L::K + (16 * ks + trow) * L::KP + tcol + c0 * 2 + i * 16 + 32);
+                    mma16816(acc[0], rh[ks], b0[0], b0[1]);
+                    mma16816(acc[1], rh[ks], b0[2], b0[3]);
+                    mma16816(acc[2], rh[ks], b1[0], b1[1]);
+                    mma16816(acc[3], rh[ks], b1[2], b1[3]);
+                    mma16816(acc[0], rl[ks], b0[0], b0[1]);
+                    mma16816(acc[1], rl[ks], b0[2], b0[3]);
+                    mma16816(acc[2], rl[ks], b1[0], b1[1]);
+                    mma16816(acc[3], rl[ks], b1[2], b1[3]);
                 }
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    z[i + t][0] = fmaf(gend, z[i + t][0], iu0 * (acc[t][0] + ac2[t][0]));
-                    z[i + t][1] = fmaf(gend, z[i + t][1], iu0 * (acc[t][1] + ac2[t][1]));
-                    z[i + t][2] = fmaf(gend, z[i + t][2], iu1 * (acc[t][2] + ac2[t][2]));
-                    z[i + t][3] = fmaf(gend, z[i + t][3], iu1 * (acc[t][3] + ac2[t][3]));
+                for (int t = 0; t < 4; ++t) {
+                    z[i + t][0] = fmaf(iu0, acc[t][0], z[i + t][0]);
+                    z[i + t][1] = fmaf(iu0, acc[t][1], z[i + t][1]);
+                    z[i + t][2] = fmaf(iu1, acc[t][2], z[i + t][2]);
+                    z[i + t][3] = fmaf(iu1, acc[t][3], z[i + t][3]);
+                    zm0 = fmaxf(zm0, fmaxf(fabsf(z[i + t][0]), fabsf(z[i + t][1])));
+                    zm1 = fmaxf(zm1, fmaxf(fabsf(z[i + t][2]), fabsf(z[i + t][3])));
                 }
             }
         }
