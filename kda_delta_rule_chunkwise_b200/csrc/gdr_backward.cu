@@ -40,7 +40,9 @@ struct AdjointArgs {
     const float *dstate_out;
     __nv_bfloat16 *dv_out;
     float *dstate_in;
-    float *e_out, *blocks, *tops;
+    float *e_out;
+    unsigned char *blocks;
+    float *scales;
 };
 
 // Warps, stages and the two halves of KS = 2 as in gdr_chain_kernel; chunks from last to first.
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32)
     }
     const int nrow = (lane & 7) + (lane >> 4) * 8, ncol = ((lane >> 3) & 1) * 16;
     const int trow = lane & 15, tcol = (lane >> 4) * 16;
-    unsigned char *out_tile = smem + M::OUT + group * kChunk * M::OP;
+    unsigned char *out_tile = smem + M::OUT + warp * kChunk * M::OP;
     const int64_t vstride = (int64_t)a.H * a.dv;
     bool ok = true;
     uint32_t pk[4][2];   // a chunk's dV in bf16; with KS = 2 written inside the next chunk
@@ -117,17 +119,11 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32)
         const bool block_end = (ci & 1) == 1 || it == 0;
         const int64_t blk = (first_block(span, n) + ci / 2) * a.H + h;
 
-        if (block_end) {
-            float *dst = args.blocks + blk * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    dst[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] = z[i][x];
-        }
         float m0, m1, iz0, iz1;
         const float fz0 = row_scale(quad_max(zm0), iz0), fz1 = row_scale(quad_max(zm1), iz1);
-        if (block_end) store_top(args.tops + (blk * (a.dv / 16) + j0 / 16) * 2, fmaxf(zm0, zm1), KS, part);
+        if (block_end)
+            store_block<NC>(args.blocks + blk * DK * block_row(a.dv), args.scales + (blk * (a.dv / 16) + j0 / 16) * 2,
+                            z, fmaxf(zm0, zm1), KS, part, c0, j0, a.dv, smem + M::OUT + warp * kChunk * M::OP);
 
         ok = pipe.wait(pipe.full + st, (it / M::ST) & 1);
         if (!ok) break;
@@ -425,10 +421,13 @@ constexpr int kGradWarps = 16, kGradThreads = kGradWarps * 32;
 
 struct GradsArgs {
     const __nv_bfloat16 *q, *k, *dout, *g, *beta;
-    const float *n_in, *e_in, *s_blocks, *z_blocks, *s_tops, *z_tops;
+    const float *n_in, *e_in, *s_scales, *z_scales;
+    const unsigned char *s_blocks, *z_blocks;
     const int32_t *cu, *owners;
-    int64_t T;
+    int64_t T, blocks;
     int Hk, H;
+    uint32_t *err;
+    uint32_t epoch;
     __nv_bfloat16 *dq, *dk, *dg, *dbeta;
 };
 
@@ -444,7 +443,10 @@ struct GradsSmem {
     enum { GH = 0, GL = 1, INTO = 2, OUT = 3, BETA = 4, DBETA = 5, ROW = 6 /* 4 */, STATE = 10 /* 4 */,
            WRITE = 14 /* 4 */, COL = 18 /* 4 */, COUNT = 22 };
     static constexpr int RED = F + COUNT * kBlock * 4;
-    static constexpr int BYTES = RED + 6 * kGradWarps * 4;
+    static constexpr int SC = RED + 6 * kGradWarps * 4;   // scales of S and Z: fp32 [2][DV / 16][2], then half2
+    static constexpr int MU = SC + 2 * (DV / 16) * 2 * 4;
+    static constexpr int BAR = MU + 2 * 2 * (DV / 16) * 4 + 4 * 4;
+    static constexpr int BYTES = BAR + 16;
 };
 
 // A power of two that brings m (a tile's largest value) into [2^7, 2^8), and its inverse: a
@@ -473,6 +475,37 @@ __device__ __forceinline__ void product_nt(float (&c)[NT][4], uint32_t a, int ap
     for (int kk = 0; kk < K16; ++kk) {
         uint32_t ra[4];
         ldsm4(ra, a + kk * 32);
+#pragma unroll
+        for (int i = 0; i < NT; i += 2) {
+            uint32_t rb[4];
+            ldsm4(rb, b + i * 8 * bp + kk * 32);
+            mma16816(c[i], ra, rb[0], rb[1]);
+            mma16816(c[i + 1], ra, rb[2], rb[3]);
+        }
+    }
+}
+
+// The same with the k steps of A times mult[kk]: powers of two that bring B's parts to one scale.
+template <int NT, int K16>
+__device__ __forceinline__ void product_nt_scaled(float (&c)[NT][4], uint32_t a, int ap, uint32_t b, int bp,
+                                                  const __half2 *mult) {
+    const int lane = threadIdx.x & 31;
+    a += (lane & 15) * ap + (lane >> 4) * 16;
+    b += ((lane & 7) + (lane >> 4) * 8) * bp + ((lane >> 3) & 1) * 16;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) c[i][x] = 0.f;
+#pragma unroll 2
+    for (int kk = 0; kk < K16; ++kk) {
+        uint32_t ra[4];
+        ldsm4(ra, a + kk * 32);
+        const __half2 m = mult[kk];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const __half2 v = __hmul2(reinterpret_cast<const __half2 &>(ra[x]), m);
+            ra[x] = reinterpret_cast<const uint32_t &>(v);
+        }
 #pragma unroll
         for (int i = 0; i < NT; i += 2) {
             uint32_t rb[4];
@@ -515,27 +548,57 @@ __device__ __forceinline__ void product_add(float (&c)[NT][4], float f, uint32_t
         for (int x = 0; x < 4; ++x) c[i][x] = fmaf(f, acc[i][x], c[i][x]);
 }
 
-// One CTA per (64-token block, key head); it walks the value heads of the key head's group and
-// sums dq and dk over them in registers, in order.  Warp w has rows 16 (w % 4) .. and the quarter
-// w / 4 of the columns.
+// Items are (64-token block, key head) pairs, spread over one CTA per SM; for each the CTA walks the
+// value heads of the key head's group and sums dq and dk over them in registers, in order.  Warp w has
+// rows 16 (w % 4) .. and the quarter w / 4 of the columns.  S and Z of the next head are copied in as
+// soon as the last product with the present ones is done.
 template <int DK, int DV>
 __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a) {
     using M = GradsSmem<DK, DV>;
     constexpr int NF = DK / 32;   // column tiles of a warp in [64][DK] results
+    constexpr int G = DV / 16;    // column groups of S and Z with a scale each
     extern __shared__ __align__(128) unsigned char smem[];
     float *rows = reinterpret_cast<float *>(smem + M::F);
     float *red = reinterpret_cast<float *>(smem + M::RED);
+    float *sc = reinterpret_cast<float *>(smem + M::SC);            // [S, Z][G][2] inverse scales
+    __half2 *mult = reinterpret_cast<__half2 *>(smem + M::MU);      // [S, Z][2][G], relative to the largest
+    float *top = reinterpret_cast<float *>(smem + M::MU + 2 * 2 * G * 4);   // [S, Z][2]: the largest
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + M::BAR);
+    volatile uint32_t *abort = reinterpret_cast<volatile uint32_t *>(bar + 1);
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wm = warp & 3, wn = warp >> 2, r0 = lane >> 2, cc = 2 * (lane & 3);
-    const int hk = blockIdx.x % a.Hk;
-    const int64_t slot = blockIdx.x / a.Hk;
+    const int group = a.H / a.Hk;
+    const int64_t items = a.blocks * a.Hk;
 
-    const int n = a.owners[slot];   // the sequence that this block belongs to, or none
-    if (n < 0) return;
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        mbar_fence_init();
+        *abort = 0u;
+    }
+    __syncthreads();
+    // the next item at or behind `i` whose block belongs to a sequence
+    auto next_item = [&](int64_t i) {
+        while (i < items && a.owners[i / a.Hk] < 0) i += gridDim.x;
+        return i;
+    };
+    auto fetch_states = [&](int64_t i, int hg) {   // one thread
+        const int64_t unit = (i / a.Hk) * a.H + (i % a.Hk) * group + hg;
+        mbar_arrive_expect_tx(bar, 2 * DK * M::VP);
+        bulk_load(sb + M::S, a.s_blocks + unit * DK * M::VP, DK * M::VP, bar);
+        bulk_load(sb + M::Z, a.z_blocks + unit * DK * M::VP, DK * M::VP, bar);
+    };
+    uint32_t parity = 0;
+    int64_t item = next_item(blockIdx.x);
+    if (tid == 0 && item < items) fetch_states(item, 0);
+    for (; item < items;) {
+    const int64_t after = next_item(item + gridDim.x);
+    const int hk = (int)(item % a.Hk);
+    const int64_t slot = item / a.Hk;
+    const int n = a.owners[slot];
     const Span span = sequence_span(a.cu, n, a.T);
     const int blk = (int)(slot - first_block(span, n));
-        const int valid = min(kBlock, span.len - blk * kBlock);
+    const int valid = min(kBlock, span.len - blk * kBlock);
     const int64_t row0 = span.row + (int64_t)blk * kBlock;
 
     // largest value over the CTA; each call has its own slots of `red`
@@ -614,7 +677,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
 #pragma unroll
         for (int x = 0; x < 4; ++x) dq[i][x] = dk[i][x] = 0.f;
 
-    const int group = a.H / a.Hk;
 #pragma unroll 1
     for (int hg = 0; hg < group; ++hg) {
         const int h = hk * group + hg;
@@ -653,32 +715,36 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
         const float so = load_bf16(DVc{}, a.dout + voff, vstride, M::DO, M::VP, 2);
         const float sn = load_f32(a.n_in + voff, vstride, M::NN, 3);
         const float se = load_f32(a.e_in + voff, vstride, M::E, 4);
-        // S and Z with scales from their stored largest values, and <S, Z>
-        float ss, sz, dot = 0.f;
+        // S and Z: their scales, and <S, Z>
+        const int64_t unit = slot * a.H + h;
+        if (tid < 4 * G) sc[tid] = tid < 2 * G ? a.s_scales[unit * 2 * G + tid] : a.z_scales[unit * 2 * G + tid - 2 * G];
+        __syncthreads();
+        if (tid < 4) {   // the largest of a half, and the groups' scales relative to it
+            const int which = tid >> 1, half = tid & 1;
+            float t = 0.f;
+            for (int g = 0; g < G; ++g) t = fmaxf(t, sc[(which * G + g) * 2 + half]);
+            top[tid] = t;
+            for (int g = 0; g < G; ++g)
+                mult[tid * G + g] = __float2half2_rn(__fdividef(sc[(which * G + g) * 2 + half], t));
+        }
+        if (!warp_wait(bar, parity, a.err, a.epoch, abort)) return;
+        parity ^= 1u;
         {
-            const int64_t unit = slot * a.H + h;
-            float ms = 0.f, mz = 0.f;
-            if (lane < DV / 8) {
-                ms = a.s_tops[unit * (DV / 8) + lane];
-                mz = a.z_tops[unit * (DV / 8) + lane];
-            }
+            float dot = 0.f;
+#pragma unroll 2
+            for (int x = tid; x < DK * DV / 8; x += kGradThreads) {
+                const int c = x / (DV / 8), j = x % (DV / 8), half = c >= DK / 2;
+                const uint4 u = *reinterpret_cast<const uint4 *>(smem + M::S + c * M::VP + j * 16);
+                const uint4 v = *reinterpret_cast<const uint4 *>(smem + M::Z + c * M::VP + j * 16);
+                const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+                float d = 0.f;
 #pragma unroll
-            for (int x = 16; x > 0; x >>= 1) {
-                ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, x));
-                mz = fmaxf(mz, __shfl_xor_sync(0xffffffffu, mz, x));
-            }
-            const float fs = tile_scale(ms, ss), fz = tile_scale(mz, sz);
-            const float4 *s4 = reinterpret_cast<const float4 *>(a.s_blocks + unit * DK * DV);
-            const float4 *z4 = reinterpret_cast<const float4 *>(a.z_blocks + unit * DK * DV);
-#pragma unroll 8
-            for (int x = tid; x < DK * DV / 4; x += kGradThreads) {
-                const float4 u = __ldcs(s4 + x), v = __ldcs(z4 + x);
-                dot += u.x * v.x + u.y * v.y + (u.z * v.z + u.w * v.w);
-                const int c = x / (DV / 4), j = x % (DV / 4);
-                *reinterpret_cast<uint2 *>(smem + M::S + c * M::VP + j * 8) =
-                    make_uint2(pack_half(u.x * fs, u.y * fs), pack_half(u.z * fs, u.w * fs));
-                *reinterpret_cast<uint2 *>(smem + M::Z + c * M::VP + j * 8) =
-                    make_uint2(pack_half(v.x * fz, v.y * fz), pack_half(v.z * fz, v.w * fz));
+                for (int e = 0; e < 4; ++e) {
+                    const float2 p = __half22float2(reinterpret_cast<const __half2 &>(uu[e]));
+                    const float2 q = __half22float2(reinterpret_cast<const __half2 &>(vv[e]));
+                    d = fmaf(p.x, q.x, fmaf(p.y, q.y, d));
+                }
+                dot += d * sc[(j / 2) * 2 + half] * sc[(G + j / 2) * 2 + half];
             }
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
@@ -741,6 +807,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
         {
             float f[NF][4], state[2] = {0.f, 0.f}, write[2] = {0.f, 0.f};
             const uint32_t bs = sb + M::S + wn * NF * 8 * M::VP, bz = sb + M::Z + wn * NF * 8 * M::VP;
+            const int half = wn >> 1;   // of the channels: this warp's columns
+            const float ss = top[half], sz = top[2 + half];
+            const __half2 *ms = mult + half * G, *mz = mult + (2 + half) * G;
             // dot of the rows of f with the rows of a [64][DK] tile in shared memory
             auto row_dot = [&](int tile, float wa, float wb, float (&s)[2]) {
                 float x0 = 0.f, x1 = 0.f;
@@ -764,14 +833,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
                     acc[i][3] = fmaf(wb, f[i][3], acc[i][3]);
                 }
             };
-            product_nt<NF, DV / 16>(f, sb + M::DO + wm * 16 * M::VP, M::VP, bs, M::VP);
+            product_nt_scaled<NF, DV / 16>(f, sb + M::DO + wm * 16 * M::VP, M::VP, bs, M::VP, ms);
             add(dq, ia * so * ss, ib * so * ss);
             row_dot(M::Q, ia * so * ss * sq, ib * so * ss * sq, state);
-            product_nt<NF, DV / 16>(f, sb + M::E + wm * 16 * M::VP, M::VP, bs, M::VP);
+            product_nt_scaled<NF, DV / 16>(f, sb + M::E + wm * 16 * M::VP, M::VP, bs, M::VP, ms);
             add(dk, -ia * ba * se * ss, -ib * bb * se * ss);
             row_dot(M::K, -ia * ba * se * ss * sk, -ib * bb * se * ss * sk, state);
             const float oa = rows[M::OUT * kBlock + ra] * ba, ob = rows[M::OUT * kBlock + rb] * bb;
-            product_nt<NF, DV / 16>(f, sb + M::NN + wm * 16 * M::VP, M::VP, bz, M::VP);
+            product_nt_scaled<NF, DV / 16>(f, sb + M::NN + wm * 16 * M::VP, M::VP, bz, M::VP, mz);
             add(dk, oa * sn * sz, ob * sn * sz);
             row_dot(M::K, oa * sn * sz * sk, ob * sn * sz * sk, write);
 #pragma unroll
@@ -786,7 +855,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
                 }
             }
         }
+        fence_proxy_async_shared();   // S and Z have been read: the next ones may come
         __syncthreads();
+        if (tid == 0) {
+            if (hg + 1 < group) fetch_states(item, hg + 1);
+            else if (after < items) fetch_states(after, 0);
+        }
         // dP and dA are lower triangular: rows 16 wm need columns up to 16 wm + 15, and the
         // transposed products rows from 16 wm
         const float up1 = so * sn / kDown, up2 = se * sn / kDown;
@@ -840,6 +914,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
             *reinterpret_cast<__nv_bfloat162 *>(a.dq + at) = __floats2bfloat162_rn(dq[i][x], dq[i][x + 1]);
             *reinterpret_cast<__nv_bfloat162 *>(a.dk + at) = __floats2bfloat162_rn(dk[i][x], dk[i][x + 1]);
         }
+    item = after;
+    __syncthreads();   // K and Q have been read
+    }
 }
 
 // ---------------------------------------------------------------- launches
@@ -867,7 +944,8 @@ static cudaError_t launch_grads_t(const GradsArgs &a, int64_t blocks, cudaStream
     cudaError_t e = cudaFuncSetAttribute(gdr_grads_kernel<DK, DV>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    gdr_grads_kernel<DK, DV><<<(unsigned)(blocks * a.Hk), kGradThreads, bytes, st>>>(a);
+    const int64_t items = blocks * a.Hk;
+    gdr_grads_kernel<DK, DV><<<(unsigned)(items < 148 ? items : 148), kGradThreads, bytes, st>>>(a);
     e = cudaGetLastError();
     Profiler::mark(st);
     return e;
@@ -882,7 +960,7 @@ size_t gdr_backward_workspace_bytes(int64_t rows, int N, int Hk, int H, int dk, 
     using namespace gdr;
     if (!bf16) return token_backward_workspace_bytes(rows, N, H, dk, dv);
     const size_t slots = (size_t)block_slots(rows, N) * H;
-    return 2 * (up256((size_t)rows * H * dv * 4) + up256(slots * dk * dv * 4) + up256(slots * (dv / 8) * 4)) +
+    return 2 * (up256((size_t)rows * H * dv * 4) + up256(slots * dk * block_row(dv)) + up256(slots * (dv / 8) * 4)) +
            up256(slots / H * 4) + gdr_image_bytes(rows, N, Hk, H, dk, true);
 }
 
@@ -901,10 +979,10 @@ cudaError_t launch_gdr_backward(const GdrArgs &p, const GdrGrads &g, int64_t row
     GdrBackwardSpace s;
     s.n = take((size_t)rows * p.H * p.dv * 4);
     s.e = take((size_t)rows * p.H * p.dv * 4);
-    s.s_blocks = take(slots * p.dk * p.dv * 4);
-    s.z_blocks = take(slots * p.dk * p.dv * 4);
-    s.s_tops = take(slots * (p.dv / 8) * 4);
-    s.z_tops = take(slots * (p.dv / 8) * 4);
+    s.s_blocks = reinterpret_cast<unsigned char *>(take(slots * p.dk * block_row(p.dv)));
+    s.z_blocks = reinterpret_cast<unsigned char *>(take(slots * p.dk * block_row(p.dv)));
+    s.s_scales = take(slots * (p.dv / 8) * 4);
+    s.z_scales = take(slots * (p.dv / 8) * 4);
     s.owners = reinterpret_cast<int32_t *>(take(slots / p.H * 4));
     cudaError_t e = cudaMemsetAsync(s.owners, 0xff, slots / p.H * 4, st);
     if (e != cudaSuccess) return e;
@@ -915,11 +993,12 @@ cudaError_t launch_gdr_backward(const GdrArgs &p, const GdrGrads &g, int64_t row
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)p.N * p.H;
     AdjointArgs a{{m.keys, m.adjoint, p.cu_seqlens, m.order, p.T, p.Hk, p.H, p.dv, p.err, p.epoch},
-                  g.dstate_out, (bf *)g.dv, g.dstate_in, s.e, s.z_blocks, s.z_tops};
+                  g.dstate_out, (bf *)g.dv, g.dstate_in, s.e, s.z_blocks, s.z_scales};
     e = p.dk == 64 ? launch_adjoint_d<64>(a, g.dout, rows, units, st) : launch_adjoint_d<128>(a, g.dout, rows, units, st);
     if (e != cudaSuccess) return e;
     GradsArgs b{(const bf *)p.q, (const bf *)p.k, (const bf *)g.dout, (const bf *)p.g, (const bf *)p.beta,
-                s.n, s.e, s.s_blocks, s.z_blocks, s.s_tops, s.z_tops, p.cu_seqlens, s.owners, p.T, p.Hk, p.H,
+                s.n, s.e, s.s_scales, s.z_scales, s.s_blocks, s.z_blocks, p.cu_seqlens, s.owners, p.T,
+                block_slots(rows, p.N), p.Hk, p.H, p.err, p.epoch,
                 (bf *)g.dq, (bf *)g.dk, (bf *)g.dg, (bf *)g.dbeta};
     const int64_t blocks = block_slots(rows, p.N);
     if (p.dk == 64) return p.dv == 64 ? launch_grads_t<64, 64>(b, blocks, st) : launch_grads_t<64, 128>(b, blocks, st);

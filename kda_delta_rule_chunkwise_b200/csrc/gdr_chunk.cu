@@ -36,8 +36,8 @@ struct ChainArgs {
     __nv_bfloat16 *o;       // prefill
     float *state_out;       // prefill
     float *n_out;           // recomputation: N [rows, H, dv]
-    float *blocks;          // recomputation: state before each 64-token block [.., H, dk, dv]
-    float *tops;            // recomputation: largest |state| of each block's parts [.., H, dv/16, 2]
+    unsigned char *blocks;  // recomputation: state before each 64-token block [.., H] (store_block)
+    float *scales;          // recomputation: their inverse scales [.., H, dv/16, 2]
     int32_t *owners;        // recomputation: the sequence of each block
 };
 
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
     // per-lane parts of the ldmatrix addresses
     const int nrow = (lane & 7) + (lane >> 4) * 8, ncol = ((lane >> 3) & 1) * 16;   // [n][k] tiles
     const int trow = lane & 15, tcol = (lane >> 4) * 16;                            // [k][n] tiles
-    unsigned char *out_tile = smem + M::OUT + group * kChunk * M::OP;
+    unsigned char *out_tile = smem + M::OUT + warp * kChunk * M::OP;
     const int64_t vstride = (int64_t)a.H * a.dv;
     ChunkOut out;   // KS = 1: this warp writes the outputs itself
     bool ok = true;
@@ -221,13 +221,8 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
         const float fs0 = row_scale(quad_max(sm0), is0), fs1 = row_scale(quad_max(sm1), is1);
         if (REC && (ci & 1) == 0) {
             const int64_t blk = (first_block(span, n) + ci / 2) * a.H + h;
-            float *dst = args.blocks + blk * DK * a.dv + (int64_t)(c0 + tc) * a.dv + j0 + jr;
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    dst[(int64_t)(8 * i + (x & 1)) * a.dv + (x >> 1) * 8] = s[i][x];
-            store_top(args.tops + (blk * (a.dv / 16) + j0 / 16) * 2, fmaxf(sm0, sm1), KS, part);
+            store_block<NC>(args.blocks + blk * DK * block_row(a.dv), args.scales + (blk * (a.dv / 16) + j0 / 16) * 2,
+                            s, fmaxf(sm0, sm1), KS, part, c0, j0, a.dv, out_tile);
         }
         ok = pipe.wait(pipe.full + st, (ci / M::ST) & 1);
         if (!ok) break;
@@ -494,7 +489,7 @@ cudaError_t launch_gdr_prefill(const GdrArgs &p, void *workspace, cudaStream_t s
 
 cudaError_t launch_gdr_recompute(const GdrArgs &p, const GdrImages &m, const GdrBackwardSpace &w, cudaStream_t st) {
     gdr::ChainArgs a{{m.keys, m.forward, p.cu_seqlens, m.order, p.T, p.Hk, p.H, p.dv, p.err, p.epoch},
-                     p.state_in, nullptr, nullptr, w.n, w.s_blocks, w.s_tops, w.owners};
+                     p.state_in, nullptr, nullptr, w.n, w.s_blocks, w.s_scales, w.owners};
     const int64_t units = (int64_t)p.N * p.H;
     return p.dk == 64 ? gdr::launch_chain_d<64, true>(a, p.v, p.rows, units, st)
                       : gdr::launch_chain_d<128, true>(a, p.v, p.rows, units, st);

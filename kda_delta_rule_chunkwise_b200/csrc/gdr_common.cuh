@@ -105,13 +105,41 @@ __device__ __forceinline__ float quad_max(float m) {
     return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
-// The largest of a warp's values (m: this lane's), for its part of a stored block: two slots,
-// one for each half of the channels (both written where one warp has them all).
-__device__ __forceinline__ void store_top(float *dst, float m, int halves, int part) {
+// The state before (or the adjoint state behind) a 64-token block as the block kernel reads it: fp16
+// [DK][dv] in padded rows, each warp's part scaled by a power of two; the inverse scales lie beside it
+// in [dv / 16][2] slots, one for each half of the channels (both written where one warp has them all).
+__host__ __device__ constexpr int block_row(int dv) { return dv * 2 + 16; }
+// One chain warp's part: channels c0 .. c0 + 8 NC - 1 of columns j0 .. j0 + 15.  m: this lane's largest
+// magnitude.  `tile`: 32 rows of shared memory of this warp's own, at a pitch of 48 bytes.
+template <int NC>
+__device__ __forceinline__ void store_block(unsigned char *image, float *scale, const float (&s)[NC][4], float m,
+                                            int halves, int part, int c0, int j0, int dv, unsigned char *tile) {
+    constexpr int OP = 48;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    const int lane = threadIdx.x & 31;
-    if (halves == 2 ? lane == 0 : lane < 2) dst[halves == 2 ? part : lane] = m;
+    float inv;
+    const float f = row_scale(m, inv);
+    if (halves == 2 ? lane == 0 : lane < 2) scale[halves == 2 ? part : lane] = inv;
+    const int nrow = (lane & 7) + (lane >> 4) * 8, ncol = ((lane >> 3) & 1) * 16;
+#pragma unroll
+    for (int i = 0; i < NC; i += 4) {
+        __syncwarp();   // the rows before have been read
+#pragma unroll
+        for (int t = 0; t < 4; t += 2)
+            stsm4_t(smem_u32(tile) + (8 * t + nrow) * OP + ncol, pack_half(s[i + t][0] * f, s[i + t][1] * f),
+                    pack_half(s[i + t][2] * f, s[i + t][3] * f),
+                    pack_half(s[i + t + 1][0] * f, s[i + t + 1][1] * f),
+                    pack_half(s[i + t + 1][2] * f, s[i + t + 1][3] * f));
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int c = u * 16 + (lane >> 1);
+            *reinterpret_cast<uint4 *>(image + (c0 + 8 * i + c) * block_row(dv) + j0 * 2 + (lane & 1) * 16) =
+                *reinterpret_cast<const uint4 *>(tile + c * OP + (lane & 1) * 16);
+        }
+    }
+    __syncwarp();
 }
 
 // Zero the tokens from `valid` on in four transposed 8x8 bf16 fragments: the first two hold tokens t
@@ -269,9 +297,9 @@ struct Pipe {
     using L = Stage<DK, W, ADJ, WANT_Q>;
     static constexpr int ST = NCW == 8 ? 4 : 5;
     static constexpr int CHAIN = NCW * KS, OW = OUTW > 0 ? NCW : 0, WARPS = CHAIN + 1 + OW;
-    static constexpr int OP = 48;                         // row pitch of a 32 x 16 output tile
+    static constexpr int OP = 48;                         // row pitch of a warp's 32 x 16 output tile
     static constexpr int OUT = ST * L::BYTES;
-    static constexpr int SWAP = OUT + NCW * kChunk * OP;
+    static constexpr int SWAP = OUT + CHAIN * kChunk * OP;
     static constexpr int HAND = SWAP + (KS == 2 ? NCW * 2 * 2 * 16 * 32 * 4 : 0);
     static constexpr int BARS = HAND + OW * ST * OUTW;
     static constexpr int BYTES = BARS + (2 * ST + 2 * NCW + OW * ST) * 8 + 16;

@@ -35,8 +35,8 @@ cudaError_t launch_gdr_prefill(const GdrArgs &a, void *workspace, cudaStream_t s
 // the gradients of each block (gdr_backward.cu).
 struct GdrBackwardSpace {
     float *n, *e;                  // [rows, H, dv]
-    float *s_blocks, *z_blocks;    // [rows / 64 + N + 1, H, dk, dv]
-    float *s_tops, *z_tops;        // [rows / 64 + N + 1, H, dv / 16, 2]
+    unsigned char *s_blocks, *z_blocks;   // [rows / 64 + N + 1, H], fp16 (store_block)
+    float *s_scales, *z_scales;           // [rows / 64 + N + 1, H, dv / 16, 2]
     int32_t *owners;               // [rows / 64 + N + 1]: a block's sequence, or -1
 };
 struct GdrGrads {
