@@ -601,32 +601,51 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
     const int valid = min(kBlock, span.len - blk * kBlock);
     const int64_t row0 = span.row + (int64_t)blk * kBlock;
 
-    // largest value over the CTA; each call has its own slots of `red`
-    auto cta_max = [&](float m, int at) {
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-        if (lane == 0) red[at * kGradWarps + warp] = m;
-        __syncthreads();
-        m = red[at * kGradWarps];
-#pragma unroll
-        for (int w = 1; w < kGradWarps; ++w) m = fmaxf(m, red[at * kGradWarps + w]);
-        return m;
-    };
-    // a [64][D] bf16 tile, row r at src + r stride: scaled fp16 into shared memory
-    auto load_bf16 = [&](auto dconst, const __nv_bfloat16 *src, int64_t stride, int dst, int pitch, int at) {
+    // 64 rows of D elements as fp16 tiles with one power-of-two scale: loaded, and once the largest
+    // value over the CTA is known, stored.  All of a head's tiles are loaded before any is waited for.
+    auto load_bf16 = [&](auto dconst, auto &w, const __nv_bfloat16 *src, int64_t stride) {
         constexpr int D = decltype(dconst)::value, PER = kBlock * D / 8 / kGradThreads;
-        uint4 w[PER];
-        float m = 0.f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int x = i * kGradThreads + tid, r = x / (D / 8), c = x % (D / 8);
             w[i] = make_uint4(0u, 0u, 0u, 0u);
             if (r < valid) w[i] = __ldg(reinterpret_cast<const uint4 *>(src + r * stride) + c);
-            for (uint32_t u : {w[i].x, w[i].y, w[i].z, w[i].w})
-                m = fmaxf(m, fmaxf(fabsf(bf_lo(u)), fabsf(bf_hi(u))));
         }
-        float inv;
-        const float f = tile_scale(cta_max(m, at), inv);
+    };
+    auto load_f32 = [&](auto &w, const float *src, int64_t stride) {
+        constexpr int PER = kBlock * DV / 4 / kGradThreads;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int x = i * kGradThreads + tid, r = x / (DV / 4), c = x % (DV / 4);
+            w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < valid) w[i] = __ldcs(reinterpret_cast<const float4 *>(src + r * stride) + c);
+        }
+    };
+    // largest magnitude of this warp's values to a slot of `red`, and of the CTA's from it
+    auto max_bf16 = [&](const auto &w, int at) {
+        float m = 0.f;
+        for (const uint4 &x : w)
+            for (uint32_t u : {x.x, x.y, x.z, x.w}) m = fmaxf(m, fmaxf(fabsf(bf_lo(u)), fabsf(bf_hi(u))));
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        if (lane == 0) red[at * kGradWarps + warp] = m;
+    };
+    auto max_f32 = [&](const auto &w, int at) {
+        float m = 0.f;
+        for (const float4 &x : w)
+            m = fmaxf(m, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        if (lane == 0) red[at * kGradWarps + warp] = m;
+    };
+    auto cta_scale = [&](int at, float &inv) {
+        float m = red[at * kGradWarps + (lane & (kGradWarps - 1))];
+#pragma unroll
+        for (int x = kGradWarps / 2; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        return tile_scale(m, inv);
+    };
+    auto store_bf16 = [&](auto dconst, const auto &w, int dst, int pitch, float f) {
+        constexpr int D = decltype(dconst)::value, PER = kBlock * D / 8 / kGradThreads;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int x = i * kGradThreads + tid, r = x / (D / 8), c = x % (D / 8);
@@ -636,35 +655,31 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
                            pack_half(bf_lo(w[i].z) * f, bf_hi(w[i].z) * f),
                            pack_half(bf_lo(w[i].w) * f, bf_hi(w[i].w) * f));
         }
-        return inv;
     };
-    auto load_f32 = [&](const float *src, int64_t stride, int dst, int at) {
+    auto store_f32 = [&](const auto &w, int dst, float f) {
         constexpr int PER = kBlock * DV / 4 / kGradThreads;
-        float4 w[PER];
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int x = i * kGradThreads + tid, r = x / (DV / 4), c = x % (DV / 4);
-            w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < valid) w[i] = __ldcs(reinterpret_cast<const float4 *>(src + r * stride) + c);
-            m = fmaxf(m, fmaxf(fmaxf(fabsf(w[i].x), fabsf(w[i].y)), fmaxf(fabsf(w[i].z), fabsf(w[i].w))));
-        }
-        float inv;
-        const float f = tile_scale(cta_max(m, at), inv);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int x = i * kGradThreads + tid, r = x / (DV / 4), c = x % (DV / 4);
             *reinterpret_cast<uint2 *>(smem + dst + r * M::VP + c * 8) =
                 make_uint2(pack_half(w[i].x * f, w[i].y * f), pack_half(w[i].z * f, w[i].w * f));
         }
-        return inv;
     };
 
     using DKc = std::integral_constant<int, DK>;
     using DVc = std::integral_constant<int, DV>;
     const int64_t koff = (row0 * a.Hk + hk) * DK, kstride = (int64_t)a.Hk * DK;
-    const float sk = load_bf16(DKc{}, a.k + koff, kstride, M::K, M::KP, 0);
-    const float sq = load_bf16(DKc{}, a.q + koff, kstride, M::Q, M::KP, 1);
+    float sk, sq;
+    {
+        uint4 wk[kBlock * DK / 8 / kGradThreads], wq[kBlock * DK / 8 / kGradThreads];
+        load_bf16(DKc{}, wk, a.k + koff, kstride);
+        load_bf16(DKc{}, wq, a.q + koff, kstride);
+        max_bf16(wk, 0);
+        max_bf16(wq, 1);
+        __syncthreads();
+        store_bf16(DKc{}, wk, M::K, M::KP, cta_scale(0, sk));
+        store_bf16(DKc{}, wq, M::Q, M::KP, cta_scale(1, sq));
+    }
     __syncthreads();
     // Q K^T and K K^T, columns 16 wn ..
     float qk[2][4], kk[2][4];
@@ -680,6 +695,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
 #pragma unroll 1
     for (int hg = 0; hg < group; ++hg) {
         const int h = hk * group + hg;
+        const int64_t voff = (row0 * a.H + h) * DV, vstride = (int64_t)a.H * DV, unit = slot * a.H + h;
+        uint4 wo[kBlock * DV / 8 / kGradThreads];
+        float4 wnn[kBlock * DV / 4 / kGradThreads], we[kBlock * DV / 4 / kGradThreads];
+        load_bf16(DVc{}, wo, a.dout + voff, vstride);
+        load_f32(wnn, a.n_in + voff, vstride);
+        load_f32(we, a.e_in + voff, vstride);
+        float scale = 0.f;
+        if (tid < 4 * G) scale = tid < 2 * G ? a.s_scales[unit * 2 * G + tid] : a.z_scales[unit * 2 * G + tid - 2 * G];
         __syncthreads();   // the head before has been read
         if (warp == 0) {
             // rows 2 lane and 2 lane + 1: running sums in 64 bits
@@ -711,14 +734,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
                 rows[M::BETA * kBlock + r] = b[i];
             }
         }
-        const int64_t voff = (row0 * a.H + h) * DV, vstride = (int64_t)a.H * DV;
-        const float so = load_bf16(DVc{}, a.dout + voff, vstride, M::DO, M::VP, 2);
-        const float sn = load_f32(a.n_in + voff, vstride, M::NN, 3);
-        const float se = load_f32(a.e_in + voff, vstride, M::E, 4);
-        // S and Z: their scales, and <S, Z>
-        const int64_t unit = slot * a.H + h;
-        if (tid < 4 * G) sc[tid] = tid < 2 * G ? a.s_scales[unit * 2 * G + tid] : a.z_scales[unit * 2 * G + tid - 2 * G];
+        if (tid < 4 * G) sc[tid] = scale;
+        max_bf16(wo, 2);
+        max_f32(wnn, 3);
+        max_f32(we, 4);
         __syncthreads();
+        float so, sn, se;
+        store_bf16(DVc{}, wo, M::DO, M::VP, cta_scale(2, so));
+        store_f32(wnn, M::NN, cta_scale(3, sn));
+        store_f32(we, M::E, cta_scale(4, se));
+        // S and Z: their scales, and <S, Z>
         if (tid < 4) {   // the largest of a half, and the groups' scales relative to it
             const int which = tid >> 1, half = tid & 1;
             float t = 0.f;
