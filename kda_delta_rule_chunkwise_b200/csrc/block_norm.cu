@@ -20,64 +20,49 @@
 
 #include <type_traits>
 
+
 namespace kda {
 namespace {
 
-// V consecutive elements as loaded: 16 bytes of bf16, 32 of fp32, or one element.  They stay
-// packed in registers and are widened where they are used.
+// Eight consecutive elements as loaded: 16 bytes of bf16 or 32 of fp32.  They stay packed in
+// registers and are widened where they are used.
 template <int V, typename T>
 struct Pack {
-    static constexpr int WORDS = V == 1 ? 1 : V * (int)sizeof(T) / 4;
+    static_assert(V == 8, "vectors of eight");
+    static constexpr int WORDS = V * (int)sizeof(T) / 4;
     uint32_t w[WORDS];
+    __device__ __forceinline__ void take(int i, const uint4 &u) {
+        w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+    }
     __device__ __forceinline__ void load(const T *p) {
-        if constexpr (V == 1) {
-            w[0] = __float_as_uint(to_f32(*p));
-        } else {
 #pragma unroll
-            for (int i = 0; i < WORDS / 4; ++i) {
-                const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-                w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
-            }
-        }
+        for (int i = 0; i < WORDS / 4; ++i) take(i, __ldcs(reinterpret_cast<const uint4 *>(p) + i));
     }
     __device__ __forceinline__ void load_shared(const T *p) {   // weights: read by every row
-        if constexpr (V == 1) {
-            w[0] = __float_as_uint(to_f32(__ldg(p)));
-        } else {
 #pragma unroll
-            for (int i = 0; i < WORDS / 4; ++i) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-                w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
-            }
-        }
+        for (int i = 0; i < WORDS / 4; ++i) take(i, __ldg(reinterpret_cast<const uint4 *>(p) + i));
     }
-    __device__ __forceinline__ void load_staged(const unsigned char *tile, int c) {   // V > 1
+    __device__ __forceinline__ void load_staged(const unsigned char *tile, int c) {
         const uint4 *p = reinterpret_cast<const uint4 *>(tile + (size_t)c * sizeof(T));
 #pragma unroll
-        for (int i = 0; i < (WORDS + 3) / 4; ++i) {
-            const uint4 u = p[i];
-            w[4 * i] = u.x;
-            if constexpr (WORDS > 1) { w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w; }
-        }
+        for (int i = 0; i < WORDS / 4; ++i) take(i, p[i]);
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) w[i] = 0u;
     }
     __device__ __forceinline__ float get(int j) const {
-        if constexpr (V == 1 || sizeof(T) == 4) return __uint_as_float(w[j]);
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
         else return __uint_as_float((j & 1) ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
     }
 };
 
 template <int V, typename T>
 __device__ __forceinline__ void store(T *p, const float (&x)[V]) {
-    if constexpr (V == 1) {
-        *p = from_f32<T>(x[0]);
-    } else if constexpr (sizeof(T) == 2) {
-        uint32_t u[4];
+    if constexpr (sizeof(T) == 2) {
+        uint32_t u[V / 2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < V / 2; ++i) {
             const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
             u[i] = reinterpret_cast<const uint32_t &>(b);
         }
@@ -138,8 +123,7 @@ __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f +
 // shared memory, each filled by one bulk copy per tensor (the rows of a group are contiguous),
 // so that as many bytes are in flight as the ring holds; a stage is filled again as soon as the
 // first barrier after its reading has passed, each tensor's copy issued by a warp of its own.
-// Otherwise (widths or addresses that are no multiple of 16 bytes, rows too wide for the ring)
-// each thread loads its own elements.
+// Otherwise (rows too wide for the ring) each thread loads its own elements.
 template <int V, int NV, int TPR, int NT, bool BACK, bool STAGED, typename TX, typename T>
 struct RowSource {
     static constexpr int RPC = NT / TPR;
@@ -423,6 +407,182 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_backward_kernel(BlockNorm
     }
 }
 
+// Widths and addresses that are no multiple of 16 bytes: V = 1 or 2 elements at a time.  STASH: a row's
+// values are kept in shared memory as fp32, each thread its own columns, so that global memory is read
+// once and with all of a row's loads in flight; rows too wide for that are read again from the cache in
+// each pass.  Everything is written in the last pass, each element by the thread that has read it, so
+// outputs may lie on inputs here too.
+template <int V, typename T>
+__device__ __forceinline__ void fetch(float (&x)[V], const T *p) {
+    if constexpr (V == 1) {
+        x[0] = to_f32(*p);
+    } else if constexpr (sizeof(T) == 2) {
+        const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
+        x[0] = __uint_as_float(u << 16), x[1] = __uint_as_float(u & 0xffff0000u);
+    } else {
+        const float2 u = *reinterpret_cast<const float2 *>(p);
+        x[0] = u.x, x[1] = u.y;
+    }
+}
+template <int V, typename T>
+__device__ __forceinline__ void put(T *p, const float (&x)[V]) {
+    if constexpr (V == 1) *p = from_f32<T>(x[0]);
+    else if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x[0], x[1]);
+    else *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+}
+
+constexpr int kAnyThreads = 512, kAnyBackward = 3;   // CTAs per SM of the backward, if their sums fit
+
+// fp32 values per row and column in shared memory: x', y, sigmoid(gate), and for the backward dh, dx and
+// the sums of the two weights' gradients.
+constexpr int any_floats(bool back, bool stash) { return (back ? 2 : 0) + (stash ? (back ? 5 : 3) : 0); }
+
+template <int V, int TPR, bool BACK, bool STASH, typename TX, typename T>
+__global__ void __launch_bounds__(kAnyThreads) block_norm_any_kernel(BlockNormArgs a) {
+    constexpr int RPC = kAnyThreads / TPR;
+    extern __shared__ __align__(16) float store_[];   // [RPC][any_floats][D], each thread its own columns
+    __shared__ float red[2][2][kAnyThreads / 32];
+    __shared__ float2 red2[2][kAnyThreads / 32];
+    const int t = (threadIdx.x % TPR) * V, side = threadIdx.x / TPR, D = a.width;
+    const float inv_d = 1.f / D;
+    const T *wo = (const T *)a.w_post, *wi = (const T *)a.w_pre;
+    float *dwo = store_ + side * any_floats(BACK, STASH) * D, *dwi = dwo + D;
+    float *kx_ = dwo + (BACK ? 2 * D : 0), *ky_ = kx_ + D, *ks_ = ky_ + D, *kh_ = ks_ + D, *kd_ = kh_ + D;
+    if (BACK)
+        for (int c = t; c < D; c += TPR * V)
+            for (int j = 0; j < V; ++j) dwo[c + j] = dwi[c + j] = 0.f;
+    int turn = 0;
+    for (int64_t base = (int64_t)blockIdx.x * RPC; base < a.rows; base += (int64_t)gridDim.x * RPC, turn ^= 1) {
+        const int64_t row = base + side, at = row * D;
+        const int end = row < a.rows ? D : 0;
+        const TX *x = (const TX *)a.x + at, *dxn = a.dx_new ? (const TX *)a.dx_new + at : nullptr;
+        const T *y = (const T *)a.y + at, *gate = a.gate ? (const T *)a.gate + at : nullptr;
+        const T *dh = a.dh ? (const T *)a.dh + at : nullptr;
+        // this thread's inputs at column c, as loaded: zeros for what is missing
+        auto inputs = [&](int c, float (&xv)[V], float (&yv)[V], float (&s)[V], float (&h)[V], float (&d)[V]) {
+            fetch<V>(yv, y + c);
+            fetch<V>(xv, x + c);
+            if (gate) fetch<V>(s, gate + c);
+            if (BACK && dh) fetch<V>(h, dh + c);
+            if (BACK && dxn) fetch<V>(d, dxn + c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                s[j] = gate ? sigmoid(s[j]) : 1.f;
+                if (!(BACK && dh)) h[j] = 0.f;
+                if (!(BACK && dxn)) d[j] = 0.f;
+            }
+        };
+        float ss = 0.f;
+#pragma unroll 4
+        for (int c = t; c < end; c += TPR * V) {
+            float xv[V], yv[V], s[V], h[V], d[V];
+            if (STASH) {
+                inputs(c, xv, yv, s, h, d);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    kx_[c + j] = xv[j], ky_[c + j] = yv[j], ks_[c + j] = s[j];
+                    if (BACK) kh_[c + j] = h[j], kd_[c + j] = d[j];
+                }
+            } else {
+                fetch<V>(yv, y + c);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) ss = fmaf(yv[j], yv[j], ss);
+        }
+        const float ry = rsqrtf(row_sum<TPR>(ss, red[turn][0]) * inv_d + a.eps);
+        // x' (in place of x) and the rest at column c; FIRST: x' is not there yet
+        auto joined = [&](auto first, int c, float (&xn)[V], float (&yv)[V], float (&s)[V], float (&h)[V],
+                          float (&d)[V], float (&w)[V]) {
+            constexpr bool FIRST = decltype(first)::value;
+            fetch<V>(w, wo + c);
+            if (STASH) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    xn[j] = kx_[c + j], yv[j] = ky_[c + j], s[j] = ks_[c + j];
+                    h[j] = BACK ? kh_[c + j] : 0.f, d[j] = BACK ? kd_[c + j] : 0.f;
+                }
+            } else {
+                inputs(c, xn, yv, s, h, d);
+            }
+            if (FIRST || !STASH)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    xn[j] = fmaf(yv[j] * ry * w[j], a.scale * s[j], xn[j]);
+                    if (STASH) kx_[c + j] = xn[j];
+                }
+        };
+        using First = std::true_type;
+        using Later = std::false_type;
+        float sx = 0.f, sg = 0.f;
+#pragma unroll 2
+        for (int c = t; c < end; c += TPR * V) {
+            float xn[V], yv[V], s[V], h[V], d[V], w[V], u[V];
+            joined(First{}, c, xn, yv, s, h, d, w);
+            if (BACK) fetch<V>(u, wi + c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                sx = fmaf(xn[j], xn[j], sx);
+                if (BACK) sg = fmaf(h[j] * u[j], xn[j], sg);
+            }
+        }
+        if (!BACK) {
+            const float rx = rsqrtf(row_sum<TPR>(sx, red[turn][1]) * inv_d + a.eps);
+#pragma unroll 2
+            for (int c = t; c < end; c += TPR * V) {
+                float xn[V], yv[V], s[V], h[V], d[V], w[V], u[V];
+                joined(Later{}, c, xn, yv, s, h, d, w);
+                fetch<V>(u, wi + c);
+                put<V>((TX *)a.x_new + at + c, xn);
+#pragma unroll
+                for (int j = 0; j < V; ++j) u[j] *= xn[j] * rx;
+                put<V>((T *)a.h + at + c, u);
+            }
+            continue;
+        }
+        const float2 two = row_sum2<TPR>(sx, sg, red2[turn]);
+        const float rx = rsqrtf(two.x * inv_d + a.eps), kx = rx * rx * rx * (two.y * inv_d);
+        float sy = 0.f;
+#pragma unroll 2
+        for (int c = t; c < end; c += TPR * V) {
+            float xn[V], yv[V], s[V], h[V], d[V], w[V], u[V];
+            joined(Later{}, c, xn, yv, s, h, d, w);
+            fetch<V>(u, wi + c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float dx = d[j] + rx * (h[j] * u[j]) - kx * xn[j], dn = a.scale * dx * s[j];
+                dwi[c + j] = fmaf(h[j], xn[j] * rx, dwi[c + j]);
+                dwo[c + j] = fmaf(dn, yv[j] * ry, dwo[c + j]);
+                sy = fmaf(dn * w[j], yv[j], sy);
+            }
+        }
+        const float ky = ry * ry * ry * (row_sum<TPR>(sy, red[turn][1]) * inv_d);
+#pragma unroll 2
+        for (int c = t; c < end; c += TPR * V) {
+            float xn[V], yv[V], s[V], h[V], d[V], w[V], u[V];
+            joined(Later{}, c, xn, yv, s, h, d, w);
+            fetch<V>(u, wi + c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                d[j] = d[j] + rx * (h[j] * u[j]) - kx * xn[j];
+                const float gy = a.scale * d[j] * s[j] * w[j];
+                h[j] = gy * (1.f - s[j]) * (yv[j] * ry);
+                yv[j] = fmaf(ry, gy, -ky * yv[j]);
+            }
+            put<V>((TX *)a.dx + at + c, d);
+            if (gate) put<V>((T *)a.dgate + at + c, h);
+            put<V>((T *)a.dy + at + c, yv);
+        }
+    }
+    if (BACK) {
+        float *part = a.part + ((int64_t)blockIdx.x * RPC + side) * 2 * D;
+        for (int c = t; c < D; c += TPR * V)
+            for (int j = 0; j < V; ++j) {
+                part[c + j] = dwo[c + j];
+                part[D + c + j] = dwi[c + j];
+            }
+    }
+}
+
 // Column sums of part[parts][2 D] in a fixed order: 32 columns and 32 groups of rows per CTA.
 __global__ void __launch_bounds__(1024) block_norm_weights_kernel(const float *part, int parts,
                                                                   int D, float *dw_post,
@@ -452,6 +612,47 @@ int64_t grid_of(int64_t rows, int rpc, int ctas) {
     return all < ctas * kSMs ? all : ctas * kSMs;
 }
 
+// The weights' gradients from `parts` partial sums.
+cudaError_t launch_weights(const BlockNormArgs &a, int parts, cudaStream_t st) {
+    block_norm_weights_kernel<<<(2 * a.width + 31) / 32, 1024, 0, st>>>(a.part, parts, a.width, a.dw_post, a.dw_pre);
+    const cudaError_t e = cudaGetLastError();
+    Profiler::mark(st);
+    return e;
+}
+
+template <int V, int TPR, bool BACK, bool STASH, typename TX, typename T>
+cudaError_t launch_any_s(const BlockNormArgs &a, size_t smem, cudaStream_t st) {
+    constexpr int RPC = kAnyThreads / TPR;
+    const int64_t grid = grid_of(a.rows, RPC, BACK ? kAnyBackward : 4);
+    const auto kernel = block_norm_any_kernel<V, TPR, BACK, STASH, TX, T>;
+    if (grid > 0) {
+        const cudaError_t set =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (set != cudaSuccess) return set;
+        kernel<<<(unsigned)grid, kAnyThreads, smem, st>>>(a);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        Profiler::mark(st);
+    }
+    return BACK ? launch_weights(a, (int)grid * RPC, st) : cudaSuccess;
+}
+template <int V, int TPR, bool BACK, typename TX, typename T>
+cudaError_t launch_any_t(const BlockNormArgs &a, cudaStream_t st) {
+    const size_t row = (size_t)(kAnyThreads / TPR) * a.width * sizeof(float);
+    if (row * any_floats(BACK, true) <= 220 * 1024)
+        return launch_any_s<V, TPR, BACK, true, TX, T>(a, row * any_floats(BACK, true), st);
+    return launch_any_s<V, TPR, BACK, false, TX, T>(a, row * any_floats(BACK, false), st);
+}
+
+// The next power of two of threads to a row, 32 to 512.
+template <int V, bool BACK, typename TX, typename T>
+cudaError_t launch_any(const BlockNormArgs &a, cudaStream_t st) {
+    const int vecs = (a.width + V - 1) / V;
+    if (vecs <= 32) return launch_any_t<V, 32, BACK, TX, T>(a, st);
+    if (vecs <= 128) return launch_any_t<V, 128, BACK, TX, T>(a, st);
+    return launch_any_t<V, 512, BACK, TX, T>(a, st);
+}
+
 template <int V, int NV, int TPR, int NT, int CTAS, bool BACK, bool STAGED, typename TX, typename T>
 cudaError_t launch_s(const BlockNormArgs &a, size_t smem, cudaStream_t st) {
     constexpr int RPC = NT / TPR;
@@ -471,23 +672,19 @@ cudaError_t launch_s(const BlockNormArgs &a, size_t smem, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         Profiler::mark(st);
     }
-    if (!BACK) return cudaSuccess;
-    block_norm_weights_kernel<<<(2 * a.width + 31) / 32, 1024, 0, st>>>(a.part, (int)grid * RPC, a.width,
-                                                                       a.dw_post, a.dw_pre);
-    const cudaError_t e = cudaGetLastError();
-    Profiler::mark(st);
-    return e;
+    return BACK ? launch_weights(a, (int)grid * RPC, st) : cudaSuccess;
 }
 
-// The ring takes as many stages as fit, two at least.
+// The ring takes as many stages as fit; with one, the next rows come while the present ones are
+// worked on, since a stage is free after the first barrier.
 template <int V, int NV, int TPR, int NT, int CTAS, bool BACK, typename TX, typename T>
 cudaError_t launch_t(BlockNormArgs a, cudaStream_t st) {
-    if constexpr (V == 8) {
+    {
         const size_t stage = (size_t)(NT / TPR) * a.width *
                              ((BACK ? 2 : 1) * sizeof(TX) + ((BACK ? 2 : 1) + (a.gate ? 1 : 0)) * sizeof(T));
         const size_t fit = kRingBytes / CTAS / stage;
         a.stages = (int)(fit < (size_t)kBlockNormStages ? fit : (size_t)kBlockNormStages);
-        if (a.stages >= 2)
+        if (a.stages >= 1)
             return launch_s<V, NV, TPR, NT, CTAS, BACK, true, TX, T>(a, a.stages * stage, st);
     }
     return launch_s<V, NV, TPR, NT, CTAS, BACK, false, TX, T>(a, 0, st);
@@ -508,33 +705,39 @@ cudaError_t launch_v(const BlockNormArgs &a, cudaStream_t st) {
     if (vecs <= 256) return launch_t<V, 1, 256, NT, CTAS, BACK, TX, T>(a, st);
     if (vecs <= 512) return launch_t<V, 1, 512, NT, CTAS, BACK, TX, T>(a, st);
     if (vecs <= 1024) return launch_t<V, 2, 512, 512, 1, BACK, TX, T>(a, st);
-    if constexpr (V == 8) {
-        return launch_t<V, 4, 512, 512, 1, BACK, TX, T>(a, st);
-    } else {
-        if (vecs <= 4096) return launch_t<V, 8, 512, 512, 1, BACK, TX, T>(a, st);
-        return launch_t<V, 32, 512, 512, 1, BACK, TX, T>(a, st);
-    }
+    return launch_t<V, 4, 512, 512, 1, BACK, TX, T>(a, st);
 }
 
-bool vectors(const BlockNormArgs &a) {
-    if (a.width % 8) return false;
+// Elements that every row and tensor lets be read at a time: 8 (the ring), 2 or 1.
+int elements_at_once(const BlockNormArgs &a) {
+    uintptr_t at = 0;
     for (const void *p : {a.x, a.y, a.gate, a.w_post, a.w_pre, a.dx_new, a.dh, (const void *)a.x_new,
-                          (const void *)a.h, (const void *)a.dx, (const void *)a.dy,
-                          (const void *)a.dgate})
-        if (reinterpret_cast<uintptr_t>(p) & 15u) return false;
-    return true;
+                          (const void *)a.h, (const void *)a.dx, (const void *)a.dy, (const void *)a.dgate})
+        at |= reinterpret_cast<uintptr_t>(p);
+    if (a.width % 8 == 0 && (at & 15u) == 0) return 8;
+    return a.width % 2 == 0 && (at & 7u) == 0 ? 2 : 1;
+}
+
+template <bool BACK, typename TX, typename T>
+cudaError_t launch_types(const BlockNormArgs &a, cudaStream_t st) {
+    switch (elements_at_once(a)) {
+        case 8: return launch_v<8, BACK, TX, T>(a, st);
+        case 2: return launch_any<2, BACK, TX, T>(a, st);
+        default: return launch_any<1, BACK, TX, T>(a, st);
+    }
 }
 
 }  // namespace
 
 size_t block_norm_parts(int64_t rows, int width) {
-    // rows side by side in a CTA, for one and for eight elements a vector: the larger number
+    // rows side by side in a CTA of 512 threads, for each number of elements at once: the largest
+    static_assert(BNT == kAnyThreads, "one CTA size for all paths");
     size_t most = 0;
-    for (int v : {1, 8}) {
+    for (int v : {1, 2, 8}) {
         const int vecs = (width + v - 1) / v;
         int tpr = 32;
         while (tpr < BNT && tpr < vecs) tpr *= 2;
-        const size_t parts = (size_t)grid_of(rows, BNT / tpr, BC) * (BNT / tpr);
+        const size_t parts = (size_t)grid_of(rows, BNT / tpr, v == 8 ? BC : kAnyBackward) * (BNT / tpr);
         if (parts > most) most = parts;
     }
     return most;
@@ -543,14 +746,9 @@ size_t block_norm_parts(int64_t rows, int width) {
 cudaError_t launch_block_norm(const BlockNormArgs &a, bool x_bf16, bool bf16, bool backward,
                               cudaStream_t st) {
     using bf = __nv_bfloat16;
-    auto types = [&](auto back) {
-        constexpr bool B = decltype(back)::value;
-        const bool v = vectors(a);
-        if (x_bf16) return v ? launch_v<8, B, bf, bf>(a, st) : launch_v<1, B, bf, bf>(a, st);
-        if (bf16) return v ? launch_v<8, B, float, bf>(a, st) : launch_v<1, B, float, bf>(a, st);
-        return v ? launch_v<8, B, float, float>(a, st) : launch_v<1, B, float, float>(a, st);
-    };
-    return backward ? types(std::true_type{}) : types(std::false_type{});
+    if (x_bf16) return backward ? launch_types<true, bf, bf>(a, st) : launch_types<false, bf, bf>(a, st);
+    if (bf16) return backward ? launch_types<true, float, bf>(a, st) : launch_types<false, float, bf>(a, st);
+    return backward ? launch_types<true, float, float>(a, st) : launch_types<false, float, float>(a, st);
 }
 
 }  // namespace kda
