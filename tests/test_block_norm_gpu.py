@@ -183,3 +183,39 @@ def test_captured_beside_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(xn, want[0]) and torch.equal(h, want[1])
+
+
+@pytest.mark.parametrize("D", [64, 66, 65, 8192, 8191])
+def test_outputs_may_lie_on_inputs(D):
+    """Through the C ABI: each output on an input of its own, in both directions and on every path."""
+    lib, P = binding.load(), binding._addr
+    x, y, g, wo, wi, dxn, dh = cuda(make(5, D, F32, BF, True, seed=D))
+    want = binding.kda_block_norm(x, y, g, wo, wi, scale=0.5, eps=1e-6)
+    back = binding.kda_block_norm_backward(x, y, g, wo, wi, dxn, dh, scale=0.5, eps=1e-6)
+    st = torch.cuda.current_stream().cuda_stream
+    a, b = x.clone(), g.clone()
+    assert lib.kda_block_norm(P(a), P(y), P(b), P(wo), P(wi), 5, D, 0.5, 1e-6, 0, 1, P(a), P(b), st) == binding.KDA_OK
+    assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    a, b, c = dxn.clone(), dh.clone(), g.clone()
+    dw = torch.zeros(2, D, device="cuda")
+    need = lib.kda_block_norm_backward_workspace_bytes(5, D)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    assert lib.kda_block_norm_backward(P(x), P(y), P(c), P(wo), P(wi), P(a), P(b), 5, D, 0.5, 1e-6, 0, 1, P(a), P(b), P(c),
+                                       P(dw[0]), P(dw[1]), P(ws), need, st) == binding.KDA_OK
+    torch.cuda.synchronize()
+    for got, w in zip((a, b, c, dw[0], dw[1]), back):
+        assert torch.equal(got, w)
+
+
+def test_more_rows_than_ctas_and_rows_side_by_side():
+    for rows, D in ((1000, 40), (700, 200), (333, 1001), (5000, 24)):
+        x, y, g, wo, wi, dxn, dh = make(rows, D, BF, BF, True, seed=rows)
+        leaves = [t.double().requires_grad_(True) for t in (x, y, g, wo, wi)]
+        want = formulas(*leaves, 0.5, 1e-6)
+        grads = torch.autograd.grad(want, leaves, [dxn.double(), dh.double()])
+        d = cuda([x, y, g, wo, wi])
+        for a, b in zip(binding.kda_block_norm(*d, scale=0.5, eps=1e-6), want):
+            assert off(a, b) <= bar(BF, D)
+        back = binding.kda_block_norm_backward(*d, *cuda([dxn, dh]), scale=0.5, eps=1e-6)
+        for i, (a, b) in enumerate(zip(back, grads)):
+            assert off(a, b) <= bar(a.dtype, D, rows if i > 2 else 0), (rows, D, i)

@@ -194,3 +194,33 @@ def test_backward_captured_and_replayed():
         for _, out in graphs:
             for a, b in zip(out, want):
                 assert torch.equal(a, b)
+
+
+def test_backward_of_no_tokens_passes_the_state_gradient():
+    x, dout, ds = case(2, 0, 1, 2, 64, 64, BF, 1)
+    got = binding.kda_gdr_backward(*gpu(x[:6]), None, dout.cuda(), ds.cuda())
+    assert torch.equal(got[5].cpu(), ds) and got[0].numel() == 0
+    x, dout, ds = case(1, 4, 1, 2, 64, 64, F32, 1, [0, 0])
+    got = binding.kda_gdr_backward(*gpu(x), dout.cuda(), ds.cuda())
+    assert torch.equal(got[5].cpu(), ds) and (got[0] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_backward_of_many_short_sequences(dtype):
+    lengths = [i % 3 for i in range(700)]
+    x, dout, ds = case(1, sum(lengths), 1, 1, 64, 64, dtype, 5, lengths)
+    want = ref.backward(*x[:5], x[5], x[6], dout, ds)
+    got = binding.kda_gdr_backward(*gpu(x), dout.cuda(), ds.cuda())
+    for name, a, b in zip(NAMES, got, want):
+        assert off(a, b) <= (bar(F32, 2) if name == "dstate_in" else bar(dtype, 2)), name
+
+
+def test_backward_of_bad_offsets_stays_inside_the_tensors():
+    x, dout, ds = case(1, 128, 1, 2, 64, 64, BF, 6, [40, 40, 48])
+    d = gpu(x)
+    d[6] = torch.tensor([0, 90, 30, 500], dtype=torch.int32).cuda()
+    got = binding.kda_gdr_backward(*d, dout.cuda(), ds.cuda())
+    d[6] = torch.tensor([0, 90, 90, 128], dtype=torch.int32).cuda()
+    want = binding.kda_gdr_backward(*d, dout.cuda(), ds.cuda())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -284,3 +284,78 @@ def test_prefill_then_decode_is_one_long_prefill():
     assert off(torch.cat(parts, 1), want_o) <= tol_o(BF, 80)
     short = ref.forward(*(t[1:, :77] for t in x[:5]), x[5][1:])[1]
     assert off(s[0], want_s[0]) <= tol_state(80) and off(s[1], short[0]) <= tol_state(77)
+
+
+def test_prefill_of_no_tokens_keeps_the_states():
+    x = ref.inputs(2, 0, 1, 2, 64, 64, BF, seed=1)
+    o, s = binding.kda_gdr_chunk_prefill(*gpu(x))
+    assert o.shape == (2, 0, 2, 64) and torch.equal(s.cpu(), x[5])
+    x = ref.inputs(1, 5, 1, 2, 64, 64, BF, seed=1, lengths=[0, 0, 0])
+    o, s = binding.kda_gdr_chunk_prefill(*gpu(x))
+    assert torch.equal(s.cpu(), x[5]) and (o == 0).all()
+
+
+def test_prefill_of_many_short_sequences():
+    """More sequences than are sorted by length (4096), zero to two tokens each."""
+    lengths = [i % 3 for i in range(4200)]
+    x = ref.inputs(1, sum(lengths), 1, 1, 64, 64, BF, seed=2, lengths=lengths)
+    o, s = binding.kda_gdr_chunk_prefill(*gpu(x))
+    want_o, want_s = ref.forward(*x)
+    assert off(o, want_o) <= tol_o(BF, 2) and off(s, want_s) <= tol_state(2)
+
+
+@pytest.mark.parametrize("lengths", [[5, 300, 40, 300, 0, 1], [1] * 33 + [200]])
+def test_prefill_result_does_not_depend_on_the_neighbours(lengths):
+    """A sequence alone and packed among others: the same bits, whatever order they run in."""
+    x = ref.inputs(1, sum(lengths), 1, 2, 128, 128, BF, seed=3, lengths=lengths)
+    o, s = binding.kda_gdr_chunk_prefill(*gpu(x))
+    at = 0
+    for n, m in enumerate(lengths):
+        alone = gpu([t[:, at:at + m].contiguous() for t in x[:5]] + [x[5][n:n + 1].contiguous(), None])
+        oo, ss = binding.kda_gdr_chunk_prefill(*alone)
+        # the columns may be split over another number of warps: sums of channel halves differ in order
+        if m:
+            assert off(o[:, at:at + m], oo.cpu().double()) <= 2.0 ** -8
+        assert off(s[n], ss[0].cpu().double()) <= 1e-6
+        at += m
+
+
+def test_prefill_with_a_given_workspace_and_on_a_given_stream():
+    x = gpu(ref.inputs(1, 100, 2, 4, 128, 64, BF, seed=4, lengths=[60, 40]))
+    want = binding.kda_gdr_chunk_prefill(*x)
+    need = binding.load().kda_gdr_prefill_workspace_bytes(100, 2, 2, 4, 128, 64, binding.KDA_BF16)
+    ws = torch.full((need + 512,), 255, dtype=torch.uint8, device="cuda")     # NaN patterns; a larger one
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = binding.kda_gdr_chunk_prefill(*x, workspace=ws, stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert (ws[need:] == 255).all()
+
+
+def test_decode_captured_and_replayed_moves_the_states_on():
+    x = gpu(ref.inputs(3, 1, 1, 2, 128, 128, BF, seed=5, state=False)[:5])
+    a = torch.randn(3, 2, 128, 128, generator=torch.Generator().manual_seed(1)).cuda()
+    b = a.clone()
+    o = torch.zeros(3, 1, 2, 128, dtype=BF, device="cuda")
+    want = [binding.kda_gdr_decode(*x, a).clone() for _ in range(3)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            binding.kda_gdr_decode(*x, b, o=o)
+    torch.cuda.synchronize()
+    for w in want:
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, w)
+    assert torch.equal(a, b)
+
+
+def test_lens_and_slots_on_the_host_are_refused():
+    x = gpu(ref.inputs(2, 1, 1, 2, 64, 64, BF, seed=6, state=False)[:5])
+    s = torch.zeros(2, 2, 64, 64, device="cuda")
+    for kw in (dict(slots=torch.zeros(2, dtype=torch.int32)), dict(lens=torch.zeros(2, dtype=torch.int64, device="cuda")),
+               dict(slots=torch.zeros(3, dtype=torch.int32, device="cuda")), dict(o=torch.zeros(2, 1, 2, 64, device="cuda"))):
+        with pytest.raises(ValueError):
+            binding.kda_gdr_decode(*x, s, **kw)
