@@ -953,13 +953,14 @@ static cudaError_t launch_adjoint_t(const AdjointArgs &a, const void *dout, int6
                                st);
 }
 
-// The split of the columns by the number of units, as for the forward chain.
 template <int DK>
 static cudaError_t launch_adjoint_d(const AdjointArgs &a, const void *dout, int64_t rows, int64_t units,
                                     cudaStream_t st) {
-    if (units * (a.in.dv / 32) <= 148) return launch_adjoint_t<DK, 2, 2>(a, dout, rows, units, st);
-    if (units * (a.in.dv / 64) <= 148 || a.in.dv == 64) return launch_adjoint_t<DK, 4, 1>(a, dout, rows, units, st);
-    return launch_adjoint_t<DK, 8, 1>(a, dout, rows, units, st);
+    switch (chain_variant(units, a.in.dv, a.in.cu != nullptr)) {
+        case 22: return launch_adjoint_t<DK, 2, 2>(a, dout, rows, units, st);
+        case 41: return launch_adjoint_t<DK, 4, 1>(a, dout, rows, units, st);
+        default: return launch_adjoint_t<DK, 8, 1>(a, dout, rows, units, st);
+    }
 }
 
 template <int DK, int DV>

@@ -463,15 +463,13 @@ static cudaError_t launch_chain_t(const ChainArgs &a, const void *v, int64_t row
                                st);
 }
 
-// Columns per CTA and warps per column group.  The chain's rate is set by its warps' matrix
-// instructions (8 cycles each per SM quarter) and their latency, so with few (sequence, head)
-// units the work is spread over as many SMs and warps as there are; with many, one CTA takes all
-// columns and loads each chunk once.
 template <int DK, bool REC>
 static cudaError_t launch_chain_d(const ChainArgs &a, const void *v, int64_t rows, int64_t units, cudaStream_t st) {
-    if (units * (a.in.dv / 32) <= 148) return launch_chain_t<DK, 2, 2, REC>(a, v, rows, units, st);
-    if (units * (a.in.dv / 64) <= 148 || a.in.dv == 64) return launch_chain_t<DK, 4, 1, REC>(a, v, rows, units, st);
-    return launch_chain_t<DK, 8, 1, REC>(a, v, rows, units, st);
+    switch (chain_variant(units, a.in.dv, a.in.cu != nullptr)) {
+        case 22: return launch_chain_t<DK, 2, 2, REC>(a, v, rows, units, st);
+        case 41: return launch_chain_t<DK, 4, 1, REC>(a, v, rows, units, st);
+        default: return launch_chain_t<DK, 8, 1, REC>(a, v, rows, units, st);
+    }
 }
 
 }  // namespace gdr

@@ -384,5 +384,26 @@ inline cudaError_t launch_chain_kernel(void (*kernel)(const CUtensorMap, const A
     return e;
 }
 
+// Columns per CTA (16 NCW) and warps per 16 columns (KS) of a chain, as NCW * 10 + KS.  A round of CTAs
+// over the 148 SMs took, for 4096 tokens at dk = dv = 128 (prefill): 32 columns with two warps per 16,
+// 179 us (37 units a round at dv = 128); 64 columns with one, 216 us (74 units); 128 with one, 377 us
+// (148 units).  So 32 and 48 heads take 179 against 215 and 377 us, and 349 against 216 and 377; 96
+// heads 520 against 420 and 378; 160 heads 862 against 626 and 740.  The choice is the least of rounds
+// times that; packed sequences, which are ragged, fill the rounds' ends, so there their number is not
+// rounded up.
+inline int chain_variant(int64_t units, int dv, bool packed) {
+    struct { int columns, variant; double us; } const all[3] = {{32, 22, 179.}, {64, 41, 216.}, {128, 81, 377.}};
+    int best = 0;
+    double least = 0.;
+    for (const auto &v : all) {
+        if (v.columns > dv) break;
+        const int64_t ctas = units * (dv / v.columns);
+        double rounds = packed ? (double)ctas / 148. : (double)((ctas + 147) / 148);
+        if (rounds < 1.) rounds = 1.;
+        if (best == 0 || rounds * v.us < least) best = v.variant, least = rounds * v.us;
+    }
+    return best;
+}
+
 }  // namespace gdr
 }  // namespace kda

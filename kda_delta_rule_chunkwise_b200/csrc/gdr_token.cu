@@ -266,7 +266,9 @@ static cudaError_t launch_token_t(const GdrTokenArgs &a, cudaStream_t st) {
 
 template <int DK, typename Tin>
 static cudaError_t launch_token_d(const GdrTokenArgs &a, cudaStream_t st) {
-    // few (request, head) units: narrow slices, so that more SMs read the states
+    // few (request, head) units: narrow slices, so that more SMs read the states (32 heads of 128: 1
+    // request 9.9 us against 11.7 with whole states, 2 requests 10.0 against 10.7, 4 the same, 8
+    // requests 13.2 against 12.1)
     const int64_t units = (int64_t)a.N * a.H;
     if (units * (a.dv / 32) <= 2 * 148) return launch_token_t<DK, 32, Tin>(a, st);
     return a.dv == 64 ? launch_token_t<DK, 64, Tin>(a, st) : launch_token_t<DK, 128, Tin>(a, st);

@@ -67,7 +67,7 @@ def test_prefill_matches_the_recurrence(case, dtype):
     assert (got_o.cpu()[outside] == 7.0).all()             # rows of no sequence stay as they were
 
 
-@pytest.mark.parametrize("H,dv", [(1, 128), (37, 128), (38, 128), (75, 128), (150, 128), (75, 64), (160, 64)])
+@pytest.mark.parametrize("H,dv", [(1, 128), (37, 128), (38, 128), (75, 128), (148, 128), (150, 128), (75, 64), (160, 64)])
 def test_prefill_variants_by_unit_count(H, dv):
     """Each split of the columns over CTAs and warps (the choice goes by N H and dv)."""
     x = ref.inputs(1, 70, 1, H, 128, dv, BF, seed=H)
