@@ -229,13 +229,23 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
 
         // Y^T = S^T K'^T (two terms of S) and S^T Q'^T (the high term)
         float y[4][4], oq[4][4];
+        uint32_t high[NK][4];   // S's high terms, for Q S
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int x = 0; x < 4; ++x) y[t][x] = oq[t][x] = 0.f;
+        auto add_qs = [&](int kk) {
+            uint32_t b0[4], b1[4];
+            ldsm4(b0, sb + L::Q + nrow * L::KP + ncol + c0 * 2 + kk * 32);
+            ldsm4(b1, sb + L::Q + (nrow + 16) * L::KP + ncol + c0 * 2 + kk * 32);
+            mma16816(oq[0], high[kk], b0[0], b0[1]);
+            mma16816(oq[1], high[kk], b0[2], b0[3]);
+            mma16816(oq[2], high[kk], b1[0], b1[1]);
+            mma16816(oq[3], high[kk], b1[2], b1[3]);
+        };
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk) {
-            uint32_t hi[4], lo[4], b0[4], b1[4];
+            uint32_t(&hi)[4] = high[kk], lo[4], b0[4], b1[4];
             split_half(s[2 * kk][0] * fs0, s[2 * kk][1] * fs0, hi[0], lo[0]);
             split_half(s[2 * kk][2] * fs1, s[2 * kk][3] * fs1, hi[1], lo[1]);
             split_half(s[2 * kk + 1][0] * fs0, s[2 * kk + 1][1] * fs0, hi[2], lo[2]);
@@ -250,19 +260,11 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
             mma16816(y[1], lo, b0[2], b0[3]);
             mma16816(y[2], lo, b1[0], b1[1]);
             mma16816(y[3], lo, b1[2], b1[3]);
-            if (!REC) {
-                ldsm4(b0, sb + L::Q + nrow * L::KP + ncol + c0 * 2 + kk * 32);
-                ldsm4(b1, sb + L::Q + (nrow + 16) * L::KP + ncol + c0 * 2 + kk * 32);
-                mma16816(oq[0], hi, b0[0], b0[1]);
-                mma16816(oq[1], hi, b0[2], b0[3]);
-                mma16816(oq[2], hi, b1[0], b1[1]);
-                mma16816(oq[3], hi, b1[2], b1[3]);
-            }
+            if (!REC && KS == 1) add_qs(kk);
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             y[t][0] *= is0; y[t][1] *= is0; y[t][2] *= is1; y[t][3] *= is1;
-            oq[t][0] *= is0; oq[t][1] *= is0; oq[t][2] *= is1; oq[t][3] *= is1;
         }
         float4 *hand = KS == 2 && !REC ? reinterpret_cast<float4 *>(pipe.hand(group, st)) + lane : nullptr;
         if (KS == 2) {
@@ -274,12 +276,18 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
             for (int t = 0; t < 4; ++t) mine[t * 32] = make_float4(y[t][0], y[t][1], y[t][2], y[t][3]);
             __syncwarp();
             if (lane == 0) mbar_arrive(pipe.swapped + group * 2 + (part ^ 1));
-            if (!REC)   // this half's Q S to the output warp
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    hand[(part * 4 + t) * 32] = make_float4(oq[t][0], oq[t][1], oq[t][2], oq[t][3]);
         }
-        // what does not depend on the other half, while it is on its way
+        // what does not depend on the other half, while it is on its way: this half's Q S, for the output
+        // warp, and the operands of what follows
+        if (!REC && KS == 2)
+#pragma unroll
+            for (int kk = 0; kk < NK; ++kk) add_qs(kk);
+        if (!REC)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                oq[t][0] *= is0; oq[t][1] *= is0; oq[t][2] *= is1; oq[t][3] *= is1;
+                if (KS == 2) hand[(part * 4 + t) * 32] = make_float4(oq[t][0], oq[t][1], oq[t][2], oq[t][3]);
+            }
         uint32_t v[2][4], xh[3][4], xl[3][4];   // values; blocks (0,0) (1,0) (1,1) of X
         float2 ck[4];
 #pragma unroll
