@@ -9,6 +9,7 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -410,6 +411,8 @@ def kda_decode_step_indexed(q, k, v, g, beta, state_pool, slots, *, o=None, stre
 
 
 # ---------------------------------------------------------------- gated delta rule
+# Calls from here on also take `stream=`, a torch.cuda.Stream (see _on_stream); without it they run
+# on the current stream of the tensors' device.
 
 def _want(name, t, shape, dtype, device):
     """Refuse a tensor of another shape, type or device than the call's, or a strided one."""
@@ -430,22 +433,34 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-class _Call:
-    """The device and stream of one call: `device` is made current for its duration where it
-    is not already, and the stream is the given one or the device's current one."""
-    __slots__ = ("index", "stream", "back")
+def _on_stream(call):
+    """A call with `stream=`: all of it, the tensors that it allocates included, on that stream,
+    so that no memory changes hands between two streams behind the caller's back."""
+    @functools.wraps(call)
+    def on_stream(first, *args, stream=None, **kwargs):
+        if stream is None:
+            return call(first, *args, **kwargs)
+        if stream.device != first.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {first.device}")
+        with torch.cuda.stream(stream):
+            return call(first, *args, **kwargs)
+    return on_stream
 
-    def __init__(self, device, stream):
+
+class _Call:
+    """One call on a tensor's device: the device is made current for its duration where it is not
+    already; gives the device's current stream."""
+    __slots__ = ("index", "back")
+
+    def __init__(self, device):
         self.index = device.index
-        self.stream = (torch._C._cuda_getCurrentRawStream(self.index) if stream is None
-                       else stream.cuda_stream)
 
     def __enter__(self):
         now = torch._C._cuda_getDevice()
         self.back = -1 if now == self.index else now
         if self.back >= 0:
             torch.cuda.set_device(self.index)
-        return self.stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *_):
         if self.back >= 0:
@@ -477,14 +492,15 @@ def _gdr_shapes(q, k, v, g, beta):
     return B, T, Hk, H, dk, dv
 
 
+@_on_stream
 def kda_gdr_chunk_prefill(q, k, v, g, beta, state_in=None, cu_seqlens=None, *, o=None,
-                          state_out=None, workspace=None, want_state=True, stream=None):
+                          state_out=None, workspace=None, want_state=True):
     """Chunked prefill of the gated delta rule (one decay per value head and token).
 
     q, k: [B, T, Hk, dk]; v: [B, T, H, dv]; g, beta: [B, T, H], all bf16 or all fp32;
     H is a multiple of Hk.  state_in: [N, H, dk, dv] fp32 or None; cu_seqlens: int32 [N+1]
-    on the device or None.  Returns (o, state_out): o like v, the state fp32.  Rows of a
-    given `o` that belong to no sequence are left as they are (zeros when allocated here).
+    on the device or None.  Returns (o, state_out): o like v, the state fp32.  Rows of o that
+    belong to no sequence are not written.
     """
     B, T, Hk, H, dk, dv = _gdr_shapes(q, k, v, g, beta)
     N = B if cu_seqlens is None else cu_seqlens.numel() - 1
@@ -494,14 +510,13 @@ def kda_gdr_chunk_prefill(q, k, v, g, beta, state_in=None, cu_seqlens=None, *, o
     _want("o", o, v.shape, q.dtype, q.device)
     _want("state_out", state_out, (N, H, dk, dv), torch.float32, q.device)
     if o is None:
-        new = torch.empty if cu_seqlens is None else torch.zeros
-        o = new(v.shape, dtype=q.dtype, device=q.device)
+        o = torch.empty_like(v)
     if state_out is None and want_state:
         state_out = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
     lib = load()
     need = lib.kda_gdr_prefill_workspace_bytes(B * T, N, Hk, H, dk, dv, _DTYPE[q.dtype])
     workspace, ws_bytes = _space(workspace, need, q.device)
-    with _Call(q.device, stream) as raw_stream:
+    with _Call(q.device) as raw_stream:
         code = lib.kda_gdr_chunk_prefill(
             _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(state_in), _addr(cu_seqlens), B, T,
             N, Hk, H, dk, dv, _DTYPE[q.dtype], _addr(o), _addr(state_out), _addr(workspace), ws_bytes,
@@ -510,14 +525,14 @@ def kda_gdr_chunk_prefill(q, k, v, g, beta, state_in=None, cu_seqlens=None, *, o
     return o, state_out
 
 
-def kda_gdr_decode(q, k, v, g, beta, state, *, slots=None, lens=None, update_state=True, o=None,
-                   stream=None):
+@_on_stream
+def kda_gdr_decode(q, k, v, g, beta, state, *, slots=None, lens=None, update_state=True, o=None):
     """L tokens for each of N requests, `state` [P, H, dk, dv] fp32 updated in place.
 
     q, k: [N, L, Hk, dk]; v: [N, L, H, dv]; g, beta: [N, L, H].  slots: int32 [N], the pool
     entry of each request (distinct), or None for entry n.  lens: int32 [N], tokens that each
-    request takes, or None for all L; o of the others is left as it is (zeros when allocated
-    here).  update_state=False writes o alone.  Returns o, like v.
+    request takes, or None for all L; o of the others is not written.  update_state=False writes
+    o alone.  Returns o, like v.
     """
     N, L, Hk, H, dk, dv = _gdr_shapes(q, k, v, g, beta)
     P = state.shape[0]
@@ -526,9 +541,8 @@ def kda_gdr_decode(q, k, v, g, beta, state, *, slots=None, lens=None, update_sta
     _want("lens", lens, (N,), torch.int32, q.device)
     _want("o", o, v.shape, q.dtype, q.device)
     if o is None:
-        new = torch.empty if lens is None and slots is None else torch.zeros
-        o = new(v.shape, dtype=q.dtype, device=q.device)
-    with _Call(q.device, stream) as raw_stream:
+        o = torch.empty_like(v)
+    with _Call(q.device) as raw_stream:
         code = load().kda_gdr_decode(
             _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(state), _addr(slots), _addr(lens), N,
             P, L, Hk, H, dk, dv, _DTYPE[q.dtype], 1 if update_state else 0, _addr(o),
@@ -537,8 +551,9 @@ def kda_gdr_decode(q, k, v, g, beta, state, *, slots=None, lens=None, update_sta
     return o
 
 
+@_on_stream
 def kda_gdr_backward(q, k, v, g, beta, state_in, cu_seqlens, dout, dstate_out=None, *,
-                     want_dstate_in=True, workspace=None, stream=None):
+                     want_dstate_in=True, workspace=None):
     """Gradients of the gated delta rule: (dq, dk, dv, dg, dbeta, dstate_in), each of its input's
     type (dstate_in fp32, None unless want_dstate_in).  Inputs as for kda_gdr_chunk_prefill;
     dout like o.  Rows that belong to no sequence get zeros."""
@@ -554,7 +569,7 @@ def kda_gdr_backward(q, k, v, g, beta, state_in, cu_seqlens, dout, dstate_out=No
     ds0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device) if want_dstate_in else None
     need = int(load().kda_gdr_backward_workspace_bytes(B * T, N, Hk, H, dk, dv, _DTYPE[q.dtype]))
     workspace, ws_bytes = _space(workspace, need, q.device)
-    with _Call(q.device, stream) as raw_stream:
+    with _Call(q.device) as raw_stream:
         code = load().kda_gdr_backward(
             _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), _addr(state_in), _addr(cu_seqlens), B, T,
             N, Hk, H, dk, dv, _DTYPE[q.dtype], _addr(dout), _addr(dstate_out), _addr(dq), _addr(dk_),
@@ -566,11 +581,13 @@ def kda_gdr_backward(q, k, v, g, beta, state_in, cu_seqlens, dout, dstate_out=No
 
 class KDAGatedDeltaRule(torch.autograd.Function):
     """The gated-delta-rule prefill as a differentiable op: forward is kda_gdr_chunk_prefill,
-    backward kda_gdr_backward.  Returns (o, state_out); cu_seqlens gets no gradient."""
+    backward kda_gdr_backward.  Returns (o, state_out); cu_seqlens gets no gradient, and rows that
+    belong to no sequence are zeros in o and in the gradients."""
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, state_in=None, cu_seqlens=None):
-        o, s = kda_gdr_chunk_prefill(q, k, v, g, beta, state_in, cu_seqlens)
+        o = None if cu_seqlens is None else torch.zeros_like(v)
+        o, s = kda_gdr_chunk_prefill(q, k, v, g, beta, state_in, cu_seqlens, o=o)
         ctx.save_for_backward(q, k, v, g, beta, state_in, cu_seqlens)
         ctx.set_materialize_grads(False)
         return o, s
@@ -607,8 +624,8 @@ def _norm_shapes(x, y, gate, w_post, w_pre):
     return x.numel() // D, D
 
 
-def kda_block_norm(x, y, gate, w_post, w_pre, *, scale=1.0, eps=1e-6, x_new=None, h=None,
-                   stream=None):
+@_on_stream
+def kda_block_norm(x, y, gate, w_post, w_pre, *, scale=1.0, eps=1e-6, x_new=None, h=None):
     """Norm after a block, its gate, the scaled residual sum and the norm before the next block:
 
         x' = x + scale * sigmoid(gate) * y / rms(y) * w_post,   h = x' / rms(x') * w_pre
@@ -622,7 +639,7 @@ def kda_block_norm(x, y, gate, w_post, w_pre, *, scale=1.0, eps=1e-6, x_new=None
     _want("h", h, y.shape, y.dtype, x.device)
     x_new = torch.empty_like(x) if x_new is None else x_new
     h = torch.empty_like(y) if h is None else h
-    with _Call(x.device, stream) as raw_stream:
+    with _Call(x.device) as raw_stream:
         code = load().kda_block_norm(
             _addr(x), _addr(y), _addr(gate), _addr(w_post), _addr(w_pre), rows, D, float(scale),
             float(eps), _DTYPE[x.dtype], _DTYPE[y.dtype], _addr(x_new), _addr(h),
@@ -631,8 +648,9 @@ def kda_block_norm(x, y, gate, w_post, w_pre, *, scale=1.0, eps=1e-6, x_new=None
     return x_new, h
 
 
+@_on_stream
 def kda_block_norm_backward(x, y, gate, w_post, w_pre, dx_new, dh, *, scale=1.0, eps=1e-6,
-                            workspace=None, stream=None):
+                            workspace=None):
     """Gradients of kda_block_norm from those of its outputs (either may be None).
 
     Returns (dx, dy, dgate, dw_post, dw_pre): dx like x, dy and dgate like y (dgate None without
@@ -645,7 +663,7 @@ def kda_block_norm_backward(x, y, gate, w_post, w_pre, dx_new, dh, *, scale=1.0,
     dw = torch.empty((2, D), dtype=torch.float32, device=x.device)
     need = int(load().kda_block_norm_backward_workspace_bytes(rows, D))
     workspace, ws_bytes = _space(workspace, need, x.device)
-    with _Call(x.device, stream) as raw_stream:
+    with _Call(x.device) as raw_stream:
         code = load().kda_block_norm_backward(
             _addr(x), _addr(y), _addr(gate), _addr(w_post), _addr(w_pre), _addr(dx_new), _addr(dh), rows,
             D, float(scale), float(eps), _DTYPE[x.dtype], _DTYPE[y.dtype], _addr(dx), _addr(dy),

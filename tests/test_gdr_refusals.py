@@ -111,3 +111,11 @@ def test_binding_refuses_other_shapes_types_and_devices():
             binding._want("k", bad, q.shape, q.dtype, q.device)
     with pytest.raises(ValueError, match="contiguous"):
         binding._want("k", q.transpose(1, 2), (1, 2, 4, 64), q.dtype, q.device)
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    class Elsewhere:
+        device = torch.device("cuda", 7)
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="stream"):
+        binding.kda_gdr_chunk_prefill(q, q, q, q, q, stream=Elsewhere())
