@@ -437,13 +437,14 @@ def _on_stream(call):
     """A call with `stream=`: all of it, the tensors that it allocates included, on that stream,
     so that no memory changes hands between two streams behind the caller's back."""
     @functools.wraps(call)
-    def on_stream(first, *args, stream=None, **kwargs):
+    def on_stream(*args, stream=None, **kwargs):
         if stream is None:
-            return call(first, *args, **kwargs)
-        if stream.device != first.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {first.device}")
+            return call(*args, **kwargs)
+        for t in (*args, *kwargs.values()):
+            if isinstance(t, torch.Tensor) and t.device != stream.device:
+                raise ValueError(f"the stream is on {stream.device}, a tensor is on {t.device}")
         with torch.cuda.stream(stream):
-            return call(first, *args, **kwargs)
+            return call(*args, **kwargs)
     return on_stream
 
 

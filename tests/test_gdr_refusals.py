@@ -119,3 +119,21 @@ def test_binding_refuses_a_stream_of_another_device():
     q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="stream"):
         binding.kda_gdr_chunk_prefill(q, q, q, q, q, stream=Elsewhere())
+
+
+def test_binding_takes_every_argument_by_name():
+    """All arguments by keyword, with and without a stream: refused for the tensors' sake alone."""
+    class Elsewhere:
+        device = torch.device("cuda", 7)
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    x = torch.zeros(3, 64, dtype=torch.bfloat16)
+    calls = [(binding.kda_gdr_chunk_prefill, dict(beta=q, g=q, v=q, k=q, q=q)),
+             (binding.kda_gdr_decode, dict(q=q, k=q, v=q, g=q, beta=q, state=q)),
+             (binding.kda_gdr_backward, dict(q=q, k=q, v=q, g=q, beta=q, state_in=None, cu_seqlens=None, dout=q)),
+             (binding.kda_block_norm, dict(eps=1e-6, x=x, y=x, gate=None, w_post=x, w_pre=x)),
+             (binding.kda_block_norm_backward, dict(x=x, y=x, gate=None, w_post=x, w_pre=x, dx_new=x, dh=x))]
+    for call, arguments in calls:
+        with pytest.raises(ValueError):
+            call(**arguments)
+        with pytest.raises(ValueError, match="the stream is on"):
+            call(**arguments, stream=Elsewhere())
