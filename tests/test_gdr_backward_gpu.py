@@ -237,3 +237,15 @@ def test_backward_of_bad_offsets_stays_inside_the_tensors():
     want = binding.kda_gdr_backward(*d, dout.cuda(), ds.cuda())
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_one_token_without_a_state_has_no_decay_gradient(dtype):
+    """The decay of a sequence's first token multiplies a state of zeros: its gradient is exactly zero,
+    and dg is not formed as a difference that would leave roundings there."""
+    x, dout, ds = case(3, 1, 2, 4, 128, 128, dtype, 31, state=False)
+    got = binding.kda_gdr_backward(*gpu(x), dout.cuda(), ds.cuda())
+    assert (got[3] == 0).all()
+    want = ref.backward(*x[:5], None, None, dout, ds)
+    for name, a, b in zip(NAMES, got, want):
+        assert off(a, b) <= (bar(F32, 1) if name == "dstate_in" else bar(dtype, 1)), name
