@@ -16,8 +16,8 @@
 // (DK / RG) x 4 block of S in registers, loaded as coalesced 16-byte vectors.  The sums
 // over channels are taken over a thread's rows, over the lanes of a warp that hold the
 // same columns, and over the eight warps through shared memory, always in the same order.
-// Inputs of the next token are loaded while this one is computed; buffers alternate, so a
-// token costs two barriers.
+// Inputs of the next token are loaded while this one is computed; buffers alternate and the next
+// token's are filled between a token's two barriers, so that no third one is needed.
 #include "gdr_common.cuh"
 #include "gdr_launch.h"
 
@@ -113,8 +113,10 @@ __global__ void __launch_bounds__(256) gdr_token_kernel(GdrTokenArgs a) {
             for (int m = 16; m > 0; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
             if (lane == 0) kq[b] = d;
         }
-        if (t + 1 < len) publish(b ^ 1);
         __syncthreads();
+        // Only now have all warps updated the state of the token before, whose key lies where the next
+        // token's goes; the barrier below stands between this and its reading.
+        if (t + 1 < len) publish(b ^ 1);
         const float dec = gb[b][0];
         if (tid < DVS) {
             float pj = 0.f, yj = 0.f;

@@ -370,6 +370,20 @@ def test_decode_captured_and_replayed_moves_the_states_on():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("N,L,dv", [(200, 8, 128), (2, 64, 128), (300, 16, 64), (9, 31, 64)])
+def test_decode_of_many_tokens_is_decode_of_one_after_another(N, L, dv):
+    """All tokens in one call, many CTAs on an SM, and each in a call of its own: the same bits, every time."""
+    x = gpu(ref.inputs(N, L, 2, 4, 128, dv, BF, seed=N, state=False)[:5])
+    start = torch.randn(N, 4, 128, dv, generator=torch.Generator().manual_seed(L)).cuda()
+    one = start.clone()
+    parts = [binding.kda_gdr_decode(*[t[:, i:i + 1].contiguous() for t in x], one) for i in range(L)]
+    want = torch.cat(parts, 1)
+    for _ in range(5):
+        state = start.clone()
+        o = binding.kda_gdr_decode(*x, state)
+        assert torch.equal(o, want) and torch.equal(state, one)
+
+
 def test_lens_and_slots_on_the_host_are_refused():
     x = gpu(ref.inputs(2, 1, 1, 2, 64, 64, BF, seed=6, state=False)[:5])
     s = torch.zeros(2, 2, 64, 64, device="cuda")
