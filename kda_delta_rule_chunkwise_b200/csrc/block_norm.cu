@@ -173,6 +173,16 @@ struct RowSource {
                 "r"(dst + c.offset), "l"(c.src + (int64_t)row * c.bytes), "r"(n * c.bytes), "r"(smem_u32(bar))
             : "memory");
     }
+    // Waits, with a bound, for the groups from row `base` on that are on their way to the ring: a CTA that
+    // gives up leaves only then.  `stage`, `parity`: of group `base`.
+    static __device__ __forceinline__ void drain(const BlockNormArgs &a, int64_t base, int step, int stage,
+                                                 uint32_t parity, uint64_t *bars) {
+#pragma unroll 1
+        for (int i = 0; i < a.stages && base + (int64_t)i * step < a.rows; ++i) {
+            if (!mbar_wait(bars + stage, parity, a.err)) break;
+            if (++stage == a.stages) stage = 0, parity ^= 1u;
+        }
+    }
     // this thread's elements of its row of the group, from the stage `tile` if STAGED
     __device__ __forceinline__ void read(const BlockNormArgs &a, int row, const unsigned char *tile) {
         const int t = threadIdx.x % TPR, side = threadIdx.x / TPR;
@@ -254,7 +264,7 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_kernel(BlockNormArgs a) {
         Rows in;
         const int row = (int)base + side;
         const int64_t at = (int64_t)row * D;
-        if (STAGED && !mbar_wait_abortable(bars + stage, parity, a.err, a.epoch, &abort)) return;
+        if (STAGED) mbar_wait_abortable(bars + stage, parity, a.err, a.epoch, &abort);   // raises `abort`
         in.read(a, row, ring + stage * bytes);
         float ss = 0.f;
 #pragma unroll
@@ -263,6 +273,10 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_kernel(BlockNormArgs a) {
             for (int j = 0; j < V; ++j) ss = fmaf(in.y[i].get(j), in.y[i].get(j), ss);
         const float ry = rsqrtf(row_sum<TPR>(ss, red[turn][0]) * inv_d + a.eps) * a.scale;
         if (STAGED) {
+            if (abort) {   // the same for all threads between the row sums' barriers
+                Rows::drain(a, base, step, stage, parity, bars);
+                return;
+            }
             if (base + (int64_t)a.stages * step < a.rows)
                 Rows::issue(a, copier, (int)base + a.stages * step, ring_at + stage * bytes, bars + stage);
             if (++stage == a.stages) stage = 0, parity ^= 1u;
@@ -337,7 +351,7 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_backward_kernel(BlockNorm
         Rows in;
         const int row = (int)base + side;
         const int64_t at = (int64_t)row * D;
-        if (STAGED && !mbar_wait_abortable(bars + stage, parity, a.err, a.epoch, &abort)) return;
+        if (STAGED) mbar_wait_abortable(bars + stage, parity, a.err, a.epoch, &abort);   // raises `abort`
         in.read(a, row, ring + stage * bytes);
         const bool live = row < a.rows;
         float ss = 0.f;
@@ -347,6 +361,10 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_backward_kernel(BlockNorm
             for (int j = 0; j < V; ++j) ss = fmaf(in.y[i].get(j), in.y[i].get(j), ss);
         const float ry = rsqrtf(row_sum<TPR>(ss, red[turn][0]) * inv_d + a.eps);
         if (STAGED) {
+            if (abort) {   // the same for all threads between the row sums' barriers
+                Rows::drain(a, base, step, stage, parity, bars);
+                return;
+            }
             if (base + (int64_t)a.stages * step < a.rows)
                 Rows::issue(a, copier, (int)base + a.stages * step, ring_at + stage * bytes, bars + stage);
             if (++stage == a.stages) stage = 0, parity ^= 1u;

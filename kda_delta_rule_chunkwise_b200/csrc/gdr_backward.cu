@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
             for (int g = 0; g < G; ++g)
                 mult[tid * G + g] = __float2half2_rn(__fdividef(sc[(which * G + g) * 2 + half], t));
         }
-        if (!warp_wait(bar, parity, a.err, a.epoch, abort)) return;
+        const bool late = !warp_wait(bar, parity, a.err, a.epoch, abort);
         parity ^= 1u;
         {
             float dot = 0.f;
@@ -779,7 +779,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
             for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
             if (lane == 0) red[5 * kGradWarps + warp] = dot;
         }
-        __syncthreads();
+        if (__syncthreads_or(late)) {   // the whole CTA leaves, S and Z landed (a bounded wait)
+            if (tid == 0) mbar_wait(bar, parity ^ 1u, a.err);
+            return;
+        }
 
         const int ra = wm * 16 + r0, rb = ra + 8;   // this lane's rows
         const float ba = rows[M::BETA * kBlock + ra], bb = rows[M::BETA * kBlock + rb];

@@ -340,13 +340,16 @@ struct Pipe {
         return smem + HAND + (group * ST + s) * OUTW;
     }
 
-    // The loader warp.  REVERSE: the sequence's chunks from the last to the first.
+    // The loader warp.  REVERSE: the sequence's chunks from the last to the first.  Its lane 0 leaves only
+    // when all its copies have landed (a bounded wait), also where a wait gave up: no copy may arrive in the
+    // shared memory of a CTA that is gone.
     template <bool REVERSE>
     __device__ __forceinline__ void load(const ChainInput &a, const CUtensorMap *vmap, const Span &span, int n,
                                          int h, int hk, int column, int chunks) const {
         const int64_t slot0 = first_chunk(span, n);
-        for (int i = 0, s = 0, use = 0; i < chunks; ++i) {
-            if (use > 0 && !wait(empty + s, (use - 1) & 1)) return;
+        int i = 0;
+        for (int s = 0, use = 0; i < chunks; ++i) {
+            if (use > 0 && !wait(empty + s, (use - 1) & 1)) break;
             if ((threadIdx.x & 31) == 0) {
                 const int c = REVERSE ? chunks - 1 - i : i;
                 const uint32_t at = smem_u32(stage(s));
@@ -360,6 +363,9 @@ struct Pipe {
             __syncwarp();
             if (++s == ST) s = 0, ++use;
         }
+        if ((threadIdx.x & 31) == 0)
+            for (int c = i > ST ? i - ST : 0; c < i; ++c)
+                if (!mbar_wait(full + c % ST, (c / ST) & 1, err)) break;
     }
     // This warp is through with stage s.
     __device__ __forceinline__ void release(int s) const {

@@ -1,4 +1,4 @@
-"""The order of shared-memory accesses and barriers in the gated-delta-rule kernels, on the CPU.
+"""The order of shared-memory accesses and barriers in the gated-delta-rule and block-norm kernels, on the CPU.
 
 Whether two warps can meet in a buffer, or miss each other at a barrier, does not show in a run that
 happens to be timed well.  These tests take the accesses, barriers and waits as they stand in the
@@ -101,3 +101,16 @@ def test_two_warps_of_a_column_group_never_miss_each_other():
                 moved = True
                 todo.append((tuple(a + (i == part) for i, a in enumerate(at)), tuple(after)))
             assert moved or at == (4 * chunks, 4 * chunks), (name, "both warps wait", at, phases)
+
+
+def test_no_wait_that_gives_up_leaves_copies_behind():
+    """A kernel that copies into its shared memory waits for those copies before it leaves early."""
+    for name in ("gdr_common.cuh", "gdr_backward.cu", "block_norm.cu"):
+        assert not re.search(r"wait\w*\([^;{}]*\)\)?\s*return;", source(name)), name
+    load = block_behind(source("gdr_common.cuh"), "__device__ __forceinline__ void load(")
+    assert "mbar_wait(full + c % ST, (c / ST) & 1, err)" in load.rsplit("__syncwarp", 1)[1]
+    grads = block_behind(source("gdr_backward.cu"), "gdr_grads_kernel(GradsArgs a)")
+    assert "mbar_wait(bar, parity ^ 1u, a.err)" in block_behind(grads, "if (__syncthreads_or(late))")
+    for kernel in ("block_norm_kernel(BlockNormArgs a)", "block_norm_backward_kernel(BlockNormArgs a)"):
+        body = block_behind(source("block_norm.cu"), kernel)
+        assert "Rows::drain(a, base, step, stage, parity, bars)" in block_behind(body, "if (abort)")
