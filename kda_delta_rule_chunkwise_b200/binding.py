@@ -470,6 +470,7 @@ class _Call:
 
 def _space(workspace, need, device):
     """(workspace, its bytes): the given tensor where it is large enough, else a new one."""
+    _contig("workspace", workspace)   # its bytes are counted as one run of memory
     have = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if need and (have < need or workspace.device != device):
         return torch.empty(need, dtype=torch.uint8, device=device), need

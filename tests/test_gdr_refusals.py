@@ -137,3 +137,12 @@ def test_binding_takes_every_argument_by_name():
             call(**arguments)
         with pytest.raises(ValueError, match="the stream is on"):
             call(**arguments, stream=Elsewhere())
+
+
+@pytest.mark.parametrize("strided", [torch.zeros(1, dtype=torch.uint8).expand(4096), torch.zeros(8192, dtype=torch.uint8)[::2]])
+def test_a_workspace_with_strides_is_refused(strided):
+    """Its element count says nothing about the memory behind its address."""
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        binding._space(strided, 1024, strided.device)
+    whole = torch.zeros(4096, dtype=torch.uint8)
+    assert binding._space(whole, 1024, whole.device) == (whole, 4096) and binding._space(None, 0, whole.device) == (None, 0)
