@@ -116,6 +116,10 @@ __device__ __forceinline__ float2 row_sum2(float x, float y, float2 *red) {
     return make_float2(x, y);
 }
 
+// r^2 mean of a norm's gradient r (z - u r^2 mean(z u)), factor by factor: r mean is of z's size, while r^2
+// and r^3 alone leave the range of fp32 beside a small eps or with large rows (a row of zeros would be 0 inf).
+__device__ __forceinline__ float mean_term(float mean, float r) { return mean * r * r; }
+
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_backward_kernel(BlockNorm
                 sg = fmaf(in.dh[i].get(j) * wi[i].get(j), xn[i][j], sg);
             }
         const float2 two = row_sum2<TPR>(sx, sg, red2[turn]);
-        const float rx = rsqrtf(two.x * inv_d + a.eps), kx = rx * rx * rx * (two.y * inv_d);
+        const float rx = rsqrtf(two.x * inv_d + a.eps), kx = mean_term(two.y * inv_d, rx);
         float gy[NV][V], sy = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -391,7 +395,7 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_backward_kernel(BlockNorm
             for (int j = 0; j < V; ++j) {
                 const float h = in.dh[i].get(j), yn = in.y[i].get(j) * ry;
                 dwi[i][j] = fmaf(h, xn[i][j] * rx, dwi[i][j]);
-                dx[j] = in.dx[i].get(j) + rx * (h * wi[i].get(j)) - kx * xn[i][j];
+                dx[j] = fmaf(rx, fmaf(-kx, xn[i][j], h * wi[i].get(j)), in.dx[i].get(j));
                 const float dn = a.scale * dx[j] * s[i][j];
                 dg[j] = dn * (1.f - s[i][j]) * (yn * wo[i].get(j));
                 dwo[i][j] = fmaf(dn, yn, dwo[i][j]);
@@ -403,13 +407,13 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_backward_kernel(BlockNorm
                 if (gated) store<V>((T *)a.dgate + at + c, dg);
             }
         }
-        const float ky = ry * ry * ry * (row_sum<TPR>(sy, red[turn][1]) * inv_d);
+        const float ky = mean_term(row_sum<TPR>(sy, red[turn][1]) * inv_d, ry);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * V;
             float d[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) d[j] = fmaf(ry, gy[i][j], -ky * in.y[i].get(j));
+            for (int j = 0; j < V; ++j) d[j] = ry * fmaf(-ky, in.y[i].get(j), gy[i][j]);
             if (live && c < D) store<V>((T *)a.dy + at + c, d);
         }
     }
@@ -559,7 +563,7 @@ __global__ void __launch_bounds__(kAnyThreads) block_norm_any_kernel(BlockNormAr
             continue;
         }
         const float2 two = row_sum2<TPR>(sx, sg, red2[turn]);
-        const float rx = rsqrtf(two.x * inv_d + a.eps), kx = rx * rx * rx * (two.y * inv_d);
+        const float rx = rsqrtf(two.x * inv_d + a.eps), kx = mean_term(two.y * inv_d, rx);
         float sy = 0.f;
 #pragma unroll 2
         for (int c = t; c < end; c += TPR * V) {
@@ -568,13 +572,13 @@ __global__ void __launch_bounds__(kAnyThreads) block_norm_any_kernel(BlockNormAr
             fetch<V>(u, wi + c);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float dx = d[j] + rx * (h[j] * u[j]) - kx * xn[j], dn = a.scale * dx * s[j];
+                const float dx = fmaf(rx, fmaf(-kx, xn[j], h[j] * u[j]), d[j]), dn = a.scale * dx * s[j];
                 dwi[c + j] = fmaf(h[j], xn[j] * rx, dwi[c + j]);
                 dwo[c + j] = fmaf(dn, yv[j] * ry, dwo[c + j]);
                 sy = fmaf(dn * w[j], yv[j], sy);
             }
         }
-        const float ky = ry * ry * ry * (row_sum<TPR>(sy, red[turn][1]) * inv_d);
+        const float ky = mean_term(row_sum<TPR>(sy, red[turn][1]) * inv_d, ry);
 #pragma unroll 2
         for (int c = t; c < end; c += TPR * V) {
             float xn[V], yv[V], s[V], h[V], d[V], w[V], u[V];
@@ -582,10 +586,10 @@ __global__ void __launch_bounds__(kAnyThreads) block_norm_any_kernel(BlockNormAr
             fetch<V>(u, wi + c);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                d[j] = d[j] + rx * (h[j] * u[j]) - kx * xn[j];
+                d[j] = fmaf(rx, fmaf(-kx, xn[j], h[j] * u[j]), d[j]);
                 const float gy = a.scale * d[j] * s[j] * w[j];
                 h[j] = gy * (1.f - s[j]) * (yv[j] * ry);
-                yv[j] = fmaf(ry, gy, -ky * yv[j]);
+                yv[j] = ry * fmaf(-ky, yv[j], gy);
             }
             put<V>((TX *)a.dx + at + c, d);
             if (gate) put<V>((T *)a.dgate + at + c, h);

@@ -219,3 +219,24 @@ def test_more_rows_than_ctas_and_rows_side_by_side():
         back = binding.kda_block_norm_backward(*d, *cuda([dxn, dh]), scale=0.5, eps=1e-6)
         for i, (a, b) in enumerate(zip(back, grads)):
             assert off(a, b) <= bar(a.dtype, D, rows if i > 2 else 0), (rows, D, i)
+
+
+@pytest.mark.parametrize("D", [64, 66, 65, 16383])
+@pytest.mark.parametrize("size,eps", [(0.0, 1e-30), (0.0, 1e-36), (2.0 ** 50, 1e-6), (2.0 ** -50, 1e-36)])
+def test_gradients_of_zero_tiny_and_huge_rows(D, size, eps):
+    """rms factors whose cube is no fp32 number: 1e15 and 1e18 for rows of zeros beside a small eps, 2^-50 and
+    2^50 for huge and tiny rows (powers of two, so that the rows' digits are those of ordinary ones)."""
+    x, y, g, wo, wi, dxn, dh = make(3, D, F32, F32, True, seed=D, y_std=1.0)
+    x, y = x * size, y * size
+    small = 1e-3 if size == 0.0 else 1.0     # dy grows with the factor squared: keep it a number
+    dh = dh * small
+    scale = 0.5 * size if size else 0.5      # the block's share of x' is of x's size
+    leaves = [t.double().requires_grad_(True) for t in (x, y, g, wo, wi)]
+    want = torch.autograd.grad(formulas(*leaves, scale, eps), leaves, [torch.zeros_like(dxn).double(), dh.double()])
+    got = binding.kda_block_norm_backward(*cuda([x, y, g, wo, wi]), None, dh.cuda(), scale=scale, eps=eps)
+    _, ay = cancellations(*(t.double() for t in (x, y, g, wo, wi, torch.zeros_like(dxn), dh)), scale, eps, want[0], want[1])
+    for i, (a, b) in enumerate(zip(got, want)):
+        if float(b.abs().max()) == 0:
+            assert (a == 0).all(), i
+        else:
+            assert off(a, b) <= bar(F32, D, 3 if i > 2 else 0, max(4.0, ay)), i
