@@ -468,6 +468,30 @@ class _Call:
             torch.cuda.set_device(self.back)
 
 
+class _FirstOrder(torch.autograd.Function):
+    """The first n tensors, as functions of all of them whose derivative is refused."""
+
+    @staticmethod
+    def forward(ctx, call, n, *tensors):
+        ctx.call = call
+        return tuple(t.detach() for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.call} has no second derivative")
+
+
+def _first_order(call, grads, sources):
+    """A backward's gradients (None among them).  Where autograd records the backward itself
+    (create_graph=True) they depend on `sources` and refuse to be differentiated: the kernels give no
+    second derivative, and without this it would be dropped without a word."""
+    if not torch.is_grad_enabled():
+        return grads
+    live = [g for g in grads if g is not None]
+    kept = iter(_FirstOrder.apply(call, len(live), *live, *(t for t in sources if t is not None)))
+    return tuple(None if g is None else next(kept) for g in grads)
+
+
 def _space(workspace, need, device):
     """(workspace, its bytes): the given tensor where it is large enough, else a new one."""
     _contig("workspace", workspace)   # its bytes are counted as one run of memory
@@ -598,13 +622,15 @@ class KDAGatedDeltaRule(torch.autograd.Function):
     def backward(ctx, do, dstate):
         q, k, v, g, beta, state_in, cu = ctx.saved_tensors
         do = torch.zeros_like(v) if do is None else do.contiguous()
-        return (*kda_gdr_backward(q, k, v, g, beta, state_in, cu, do,
-                                  None if dstate is None else dstate.contiguous(),
-                                  want_dstate_in=state_in is not None), None)
+        grads = kda_gdr_backward(q, k, v, g, beta, state_in, cu, do,
+                                 None if dstate is None else dstate.contiguous(),
+                                 want_dstate_in=state_in is not None)
+        return (*_first_order("kda_gdr_autograd", grads, (q, k, v, g, beta, state_in, do, dstate)), None)
 
 
 def kda_gdr_autograd(q, k, v, g, beta, state_in=None, cu_seqlens=None):
-    """Differentiable gated-delta-rule prefill (see KDAGatedDeltaRule): (o, state_out)."""
+    """Differentiable gated-delta-rule prefill (see KDAGatedDeltaRule): (o, state_out).  Once: a
+    second derivative is refused."""
     return KDAGatedDeltaRule.apply(q, k, v, g, beta, state_in, cu_seqlens)
 
 
@@ -691,11 +717,12 @@ class KDABlockNorm(torch.autograd.Function):
         dx, dy, dgate, dwo, dwi = kda_block_norm_backward(
             x, y, gate, w_post, w_pre, None if dx_new is None else dx_new.contiguous(),
             None if dh is None else dh.contiguous(), scale=ctx.scale, eps=ctx.eps)
-        return dx, dy, dgate, dwo.to(w_post.dtype), dwi.to(w_pre.dtype), None, None
+        grads = (dx, dy, dgate, dwo.to(w_post.dtype), dwi.to(w_pre.dtype))
+        return (*_first_order("kda_block_norm_autograd", grads, (*ctx.saved_tensors, dx_new, dh)), None, None)
 
 
 def kda_block_norm_autograd(x, y, gate, w_post, w_pre, scale=1.0, eps=1e-6):
-    """Differentiable block norm (see KDABlockNorm): (x', h)."""
+    """Differentiable block norm (see KDABlockNorm): (x', h).  Once: a second derivative is refused."""
     return KDABlockNorm.apply(x, y, gate, w_post, w_pre, scale, eps)
 
 

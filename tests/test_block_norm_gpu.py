@@ -240,3 +240,14 @@ def test_gradients_of_zero_tiny_and_huge_rows(D, size, eps):
             assert (a == 0).all(), i
         else:
             assert off(a, b) <= bar(F32, D, 3 if i > 2 else 0, max(4.0, ay)), i
+
+
+def test_second_derivatives_are_refused_not_dropped():
+    """The gradients say so when a second derivative is taken through them; alone they can be used on."""
+    leaves = [t.cuda().requires_grad_(True) for t in make(3, 40, F32, F32, True)[:5]]
+    a, b = binding.kda_block_norm_autograd(*leaves)
+    grads = torch.autograd.grad(a.sum() + b.sum(), leaves, create_graph=True)
+    plain = torch.autograd.grad(sum(t.sum() for t in binding.kda_block_norm_autograd(*leaves)), leaves)
+    assert all(torch.equal(p, q) for p, q in zip(grads, plain))
+    with pytest.raises(RuntimeError, match="second derivative"):
+        (a.sum() + grads[1].square().sum()).backward()

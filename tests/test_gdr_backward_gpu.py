@@ -249,3 +249,15 @@ def test_one_token_without_a_state_has_no_decay_gradient(dtype):
     want = ref.backward(*x[:5], None, None, dout, ds)
     for name, a, b in zip(NAMES, got, want):
         assert off(a, b) <= (bar(F32, 1) if name == "dstate_in" else bar(dtype, 1)), name
+
+
+def test_second_derivatives_are_refused_not_dropped():
+    """The gradients say so when a second derivative is taken through them; alone they can be used on."""
+    x, _, _ = case(1, 20, 1, 2, 64, 64, F32, 42)
+    leaves = [t.cuda().requires_grad_(True) for t in x[:6]]
+    o, s = binding.kda_gdr_autograd(*leaves)
+    grads = torch.autograd.grad(o.sum() + s.sum(), leaves, create_graph=True)
+    plain = torch.autograd.grad(sum(t.sum() for t in binding.kda_gdr_autograd(*leaves)), leaves)
+    assert all(torch.equal(p, q) for p, q in zip(grads, plain))
+    with pytest.raises(RuntimeError, match="second derivative"):
+        (o.sum() + grads[0].square().sum()).backward()

@@ -146,3 +146,19 @@ def test_a_workspace_with_strides_is_refused(strided):
         binding._space(strided, 1024, strided.device)
     whole = torch.zeros(4096, dtype=torch.uint8)
     assert binding._space(whole, 1024, whole.device) == (whole, 4096) and binding._space(None, 0, whole.device) == (None, 0)
+
+
+def test_second_derivatives_are_refused_not_dropped(monkeypatch):
+    """With stand-ins for the kernels: y^2 and its gradient."""
+    monkeypatch.setattr(binding, "kda_block_norm", lambda x, y, *_, **__: (x * x, y * y))
+    monkeypatch.setattr(binding, "kda_block_norm_backward",
+                        lambda x, y, g, wo, wi, a, b, **_: (2 * x * a, 2 * y * b, None, wo * 0, wi * 0))
+    x, y, w = (torch.randn(4, requires_grad=True) for _ in range(3))
+    a, b = binding.kda_block_norm_autograd(x, y, None, w, w)
+    grads = torch.autograd.grad(a.sum() + b.sum(), (x, y, w), create_graph=True)
+    assert torch.equal(grads[0], 2 * x) and torch.equal(grads[1], 2 * y) and (grads[2] == 0).all()
+    with pytest.raises(RuntimeError, match="second derivative"):
+        (a.sum() + grads[1].square().sum()).backward()
+    a, b = binding.kda_block_norm_autograd(x, y, None, w, w)
+    (a.sum() + b.sum()).backward()
+    assert torch.equal(x.grad, 2 * x) and not x.grad.requires_grad
