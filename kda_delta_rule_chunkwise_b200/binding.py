@@ -605,6 +605,12 @@ def kda_gdr_backward(q, k, v, g, beta, state_in, cu_seqlens, dout, dstate_out=No
     return dq, dk_, dv_, dg, db, ds0
 
 
+def _aligned(t):
+    """t as one run of memory from a 16-byte boundary; a gradient that arrives may be a slice of another."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 class KDAGatedDeltaRule(torch.autograd.Function):
     """The gated-delta-rule prefill as a differentiable op: forward is kda_gdr_chunk_prefill,
     backward kda_gdr_backward.  Returns (o, state_out); cu_seqlens gets no gradient, and rows that
@@ -621,9 +627,9 @@ class KDAGatedDeltaRule(torch.autograd.Function):
     @staticmethod
     def backward(ctx, do, dstate):
         q, k, v, g, beta, state_in, cu = ctx.saved_tensors
-        do = torch.zeros_like(v) if do is None else do.contiguous()
-        grads = kda_gdr_backward(q, k, v, g, beta, state_in, cu, do,
-                                 None if dstate is None else dstate.contiguous(),
+        do = torch.zeros_like(v) if do is None else _aligned(do)
+        dstate = None if dstate is None else _aligned(dstate)
+        grads = kda_gdr_backward(q, k, v, g, beta, state_in, cu, do, dstate,
                                  want_dstate_in=state_in is not None)
         return (*_first_order("kda_gdr_autograd", grads, (q, k, v, g, beta, state_in, do, dstate)), None)
 

@@ -261,3 +261,17 @@ def test_second_derivatives_are_refused_not_dropped():
     assert all(torch.equal(p, q) for p, q in zip(grads, plain))
     with pytest.raises(RuntimeError, match="second derivative"):
         (o.sum() + grads[0].square().sum()).backward()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_gradients_that_arrive_at_odd_addresses(dtype):
+    """What autograd hands over may be a slice of a larger gradient, at any element."""
+    x, dout, ds = case(1, 40, 1, 2, 64, 64, dtype, 41)
+    leaves = [t.cuda().requires_grad_(True) for t in x[:6]]
+    o, s = binding.kda_gdr_autograd(*leaves)
+    head = torch.ones(3, dtype=dtype, device="cuda", requires_grad=True)
+    both, states = torch.cat([head, o.flatten()]), torch.cat([head.float(), s.flatten()])
+    torch.autograd.backward([both, states], [torch.cat([torch.zeros(3, dtype=dtype), dout.flatten()]).cuda(),
+                                             torch.cat([torch.zeros(3), ds.flatten()]).cuda()])
+    want = binding.kda_gdr_backward(*gpu(x[:6]), None, dout.cuda(), ds.cuda())
+    assert all(torch.equal(a.grad, b) for a, b in zip(leaves, want))
