@@ -397,9 +397,9 @@ KDA_API kda_status kda_chunk_prefill_host(const void *q, const void *k, const vo
  *    fp32 accuracy in either type: |error| of the final state is below 1e-6 of
  *    its norm against 64-bit arithmetic on the test inputs.
  *  - g has no lower bound: one decay per token multiplies whole rows, so no
- *    reciprocal is formed.  Values below -100 act as -100 (exp gives 0 beside
- *    any representable state), -infinity among them: such a token forgets all
- *    before it.  Values above 0 are outside the contract (fp32 uses them as
+ *    reciprocal is formed.  A token of -100 or below, -infinity among them,
+ *    forgets all before it: its decay, and that over any tokens whose g sum to
+ *    -100 or below, is exactly 0 (exp(-100) is 3.7e-44).  Values above 0 are outside the contract (fp32 uses them as
  *    given; bf16 results are unspecified).  KDA_DEBUG_CHECKS scans nothing here.
  *  - Keys need not be unit vectors (their scale is taken out per row), but bf16
  *    wants 0 <= beta |k|^2 <= 2, where no token's step enlarges the state, and

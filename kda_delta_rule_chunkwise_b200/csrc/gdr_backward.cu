@@ -733,8 +733,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
                 const double Gr = i ? G : G - (double)g[1], G2 = Gr * 1.4426950408889634074;
                 rows[M::GH * kBlock + r] = (float)G2;
                 rows[M::GL * kBlock + r] = (float)(G2 - (double)(float)G2);
-                rows[M::INTO * kBlock + r] = expf((float)Gr);
-                rows[M::OUT * kBlock + r] = expf((float)(Gend - Gr));
+                rows[M::INTO * kBlock + r] = decay((float)Gr);
+                rows[M::OUT * kBlock + r] = decay((float)(Gend - Gr));
                 rows[M::BETA * kBlock + r] = b[i];
             }
         }

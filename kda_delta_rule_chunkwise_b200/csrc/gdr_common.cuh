@@ -14,6 +14,9 @@ namespace gdr {
 
 constexpr int kChunk = 32;          // tokens per chunk of the chained kernels
 constexpr float kMinLogDecay = -100.f;
+// exp of a log-decay or a sum of them, exactly 0 from the clamp down: a token that forgets leaves nothing
+// of any state (exp(-100) is 3.7e-44, which is something beside a state of 1e38).
+__device__ __forceinline__ float decay(float g) { return g <= kMinLogDecay ? 0.f : expf(g); }
 
 // ---------------------------------------------------------------- warp products
 // D += A B with A 16x16 (row-major fragment) and B 16x8, fp16 operands, fp32 sums.

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(prep_warps<ADJ>() * 32, 1) gdr_prep_kernel(Pre
                 if (lane >= m) G += o;
             }
             const double Gend = __shfl_sync(0xffffffffu, G, 31);
-            const float into = expf((float)G), out = expf((float)(Gend - G));
+            const float into = decay((float)G), out = decay((float)(Gend - G));
             // D for this lane's rows lane/4 + 8i and columns 2(lane%4) + 8j + {0, 1}: exponents of
             // two as a high and a low part, so that far sums cancel exactly
             float D[6][4], dk[6][4];

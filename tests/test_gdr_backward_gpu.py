@@ -275,3 +275,19 @@ def test_gradients_that_arrive_at_odd_addresses(dtype):
                                              torch.cat([torch.zeros(3), ds.flatten()]).cuda()])
     want = binding.kda_gdr_backward(*gpu(x[:6]), None, dout.cuda(), ds.cuda())
     assert all(torch.equal(a.grad, b) for a, b in zip(leaves, want))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("g", [-100.0, -math.inf])
+def test_backward_through_full_forgetting_is_exactly_nothing(g, dtype):
+    """Nothing passes a token that forgets: not the state gradient behind it, however large, and not the state
+    before it; and its decay has no gradient."""
+    x, dout, ds = case(1, 40, 1, 2, 64, 64, dtype, 43)
+    x[3][:, 20] = g
+    x[5] = x[5] * 1e18                             # <S, Z> stays a number
+    got = binding.kda_gdr_backward(*gpu(x[:6]), None, torch.zeros_like(dout).cuda(), (ds * 1e18).cuda())
+    assert (got[5] == 0).all()
+    if dtype == F32:      # in bf16 dg is a sum over the block, whose other tokens' shares cancel to their roundings
+        assert (got[3][:, :21] == 0).all()
+    for a in (got[1], got[2], got[4]):
+        assert (a[:, :20] == 0).all()

@@ -391,3 +391,16 @@ def test_lens_and_slots_on_the_host_are_refused():
                dict(slots=torch.zeros(3, dtype=torch.int32, device="cuda")), dict(o=torch.zeros(2, 1, 2, 64, device="cuda"))):
         with pytest.raises(ValueError):
             binding.kda_gdr_decode(*x, s, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("g", [-100.0, -1e4, -math.inf])
+def test_full_forgetting_leaves_nothing_of_any_state(g, dtype):
+    """exp(-100) is 3.7e-44, which is something beside a large state: a token of -100 or less leaves zeros."""
+    x = ref.inputs(1, 40, 1, 2, 128, 64, dtype, seed=17)
+    x[2], x[5] = torch.zeros_like(x[2]), torch.full_like(x[5], 1e36)
+    x[3][:, 20] = g
+    o, s = binding.kda_gdr_chunk_prefill(*gpu(x))
+    assert (s == 0).all() and (o[:, 20:] == 0).all()
+    d, state = gpu([t[:, 20:23].contiguous() for t in x[:5]]), x[5].cuda()
+    assert (binding.kda_gdr_decode(*d, state) == 0).all() and (state == 0).all()
