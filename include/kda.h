@@ -410,7 +410,8 @@ KDA_API kda_status kda_chunk_prefill_host(const void *q, const void *k, const vo
  *  - q, k, v, o and the states must be 16-byte aligned (KDA_ERR_INVALID_ARG).
  *  - rows < 2^31 - 64 and N H < 2^28, else KDA_ERR_UNSUPPORTED.
  *  - A non-finite input makes the results of its own (sequence, head) unspecified,
- *    tokens before it in the same 32-token chunk among them; no other unit's.
+ *    tokens before it in the same 32-token chunk among them (in the backward any tokens
+ *    before it, and dq and dk of its key head); no other unit's.  A NaN in g shows in them.
  */
 
 /*

@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdr_grads_kernel(GradsArgs a)
                 const int r = 2 * lane + i;
                 g[i] = b[i] = 0.f;
                 if (r < valid) {
-                    g[i] = fmaxf(__bfloat162float(a.g[(row0 + r) * a.H + h]), kMinLogDecay);
+                    g[i] = log_decay(__bfloat162float(a.g[(row0 + r) * a.H + h]));
                     b[i] = __bfloat162float(a.beta[(row0 + r) * a.H + h]);
                 }
             }

@@ -14,6 +14,8 @@ namespace gdr {
 
 constexpr int kChunk = 32;          // tokens per chunk of the chained kernels
 constexpr float kMinLogDecay = -100.f;
+// A log-decay, -infinity among them, as the kernels sum it: not below the clamp.  A NaN stays one.
+__device__ __forceinline__ float log_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }
 // exp of a log-decay or a sum of them, exactly 0 from the clamp down: a token that forgets leaves nothing
 // of any state (exp(-100) is 3.7e-44, which is something beside a state of 1e38).
 __device__ __forceinline__ float decay(float g) { return g <= kMinLogDecay ? 0.f : expf(g); }

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(prep_warps<ADJ>() * 32, 1) gdr_prep_kernel(Pre
             const int h = hk * group + hg;
             float g = 0.f, b = 0.f;
             if (live) {
-                g = fmaxf(__bfloat162float(a.g[row * a.H + h]), kMinLogDecay);
+                g = log_decay(__bfloat162float(a.g[row * a.H + h]));
                 b = __bfloat162float(a.beta[row * a.H + h]);
             }
             double G = (double)g;

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(256) gdr_token_kernel(GdrTokenArgs a) {
         if (tid < DK) ks[b][tid] = in_k;
         else if (tid >= 128 && tid < 128 + DK) qs[b][tid - 128] = in_k;
         if (tid < DVS) vs[b][tid] = in_v;
-        if (tid == 0) gb[b][0] = decay(fmaxf(in_g, kMinLogDecay));
+        if (tid == 0) gb[b][0] = decay(in_g);
         if (tid == 32) gb[b][1] = in_g;
     };
     if (len > 0) {
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(128) gdr_token_prefill_kernel(GdrTokenArgs a) 
 #pragma unroll
             for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
             kq[j] = x;
-            dec[j] = decay(fmaxf(now[j].g, kMinLogDecay));
+            dec[j] = decay(now[j].g);
         }
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {

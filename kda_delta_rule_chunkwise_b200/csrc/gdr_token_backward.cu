@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256, 2) gdr_token_backward_kernel(TokenBackwar
                 if (with_grad) sm.dout[t][j] = a.dout[at];
             }
             if (tid < m) {
-                sm.a[tid] = decay(fmaxf(a.g[(row + tid) * a.H + h], kMinLogDecay));
+                sm.a[tid] = decay(a.g[(row + tid) * a.H + h]);
                 sm.beta[tid] = a.beta[(row + tid) * a.H + h];
             }
             __syncthreads();

@@ -291,3 +291,18 @@ def test_backward_through_full_forgetting_is_exactly_nothing(g, dtype):
         assert (got[3][:, :21] == 0).all()
     for a in (got[1], got[2], got[4]):
         assert (a[:, :20] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_backward_of_a_nan_decay_shows_it(dtype):
+    x, dout, ds = case(1, 100, 2, 4, 64, 64, dtype, 44, [50, 50])
+    clean = binding.kda_gdr_backward(*gpu(x), dout.cuda(), ds.cuda())
+    x[3][0, 60, 1] = float("nan")
+    got = binding.kda_gdr_backward(*gpu(x), dout.cuda(), ds.cuda())
+    assert torch.isnan(got[3][0, 50:61, 1]).any() and torch.isnan(got[5][1, 1]).any()
+    keep = [0, 2, 3]                               # other heads, and the other sequence
+    for i in (2, 3, 4):
+        assert torch.equal(got[i][0, :50], clean[i][0, :50]) and torch.equal(got[i][0, :, keep], clean[i][0, :, keep])
+    assert torch.equal(got[5][0], clean[5][0]) and torch.equal(got[5][1, keep], clean[5][1, keep])
+    for i in (0, 1):                               # key head 1 has value heads 2 and 3
+        assert torch.equal(got[i][0, :50], clean[i][0, :50]) and torch.equal(got[i][0, :, 1], clean[i][0, :, 1])

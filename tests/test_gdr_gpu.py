@@ -404,3 +404,20 @@ def test_full_forgetting_leaves_nothing_of_any_state(g, dtype):
     assert (s == 0).all() and (o[:, 20:] == 0).all()
     d, state = gpu([t[:, 20:23].contiguous() for t in x[:5]]), x[5].cuda()
     assert (binding.kda_gdr_decode(*d, state) == 0).all() and (state == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_a_nan_decay_shows_in_its_sequence_and_head(dtype):
+    x = ref.inputs(1, 100, 1, 3, 128, 64, dtype, seed=18, lengths=[40, 60])
+    clean = binding.kda_gdr_chunk_prefill(*gpu(x))
+    x[3][0, 75, 1] = float("nan")
+    o, s = binding.kda_gdr_chunk_prefill(*gpu(x))
+    assert torch.isnan(o[0, 75:, 1]).all() and torch.isnan(s[1, 1]).all()
+    keep = torch.ones(1, 100, 3, dtype=torch.bool)
+    keep[0, 72:, 1] = False                       # 72: the start of the token's chunk
+    assert torch.equal(o[keep.cuda()], clean[0][keep.cuda()])
+    assert torch.equal(s[0], clean[1][0]) and torch.equal(s[1, [0, 2]], clean[1][1, [0, 2]])
+    d, state = gpu([t[:, 74:77].contiguous() for t in x[:5]]), torch.ones(1, 3, 128, 64, device="cuda")
+    o = binding.kda_gdr_decode(*d, state)
+    assert torch.isnan(o[0, 1:, 1]).all() and torch.isnan(state[0, 1]).all()
+    assert torch.isfinite(o[0, :, [0, 2]]).all() and torch.isfinite(state[0, [0, 2]]).all() and torch.isfinite(o[0, 0]).all()
