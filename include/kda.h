@@ -79,7 +79,7 @@ typedef enum {
     KDA_ERR_UNSUPPORTED = 2,   /* valid but not implemented (e.g. dk != dv, d not 64/128) */
     KDA_ERR_CUDA = 3,          /* a CUDA runtime call or launch failed */
     KDA_ERR_TIMEOUT = 4,       /* a device-side bounded wait gave up (see kda_check_device_error) */
-    KDA_ERR_INPUT_RANGE = 5    /* debug scan only: a log-decay outside [-5, 0] or NaN (KDA_DEBUG_CHECKS) */
+    KDA_ERR_INPUT_RANGE = 5    /* debug scan only: inputs outside the contract, e.g. a log-decay outside [-5, 0] or NaN (KDA_DEBUG_CHECKS) */
 } kda_status;
 
 typedef enum {
@@ -279,7 +279,8 @@ KDA_API kda_status kda_backward(const void *q, const void *k, const void *v, con
  *                        read on the device (kda_decode_step_indexed slots, a
  *                        snapshot array too small for kda_chunk_prefill_checkpointed)
  *   KDA_ERR_INPUT_RANGE  the debug input scan (KDA_DEBUG_CHECKS=1) saw a
- *                        log-decay outside [-5, 0]
+ *                        log-decay outside [-5, 0], or inputs of the gated delta
+ *                        rule outside its contract
  * so calling it until it returns KDA_OK drains every condition.  Returns
  * KDA_ERR_CUDA if the stream reported an error, KDA_OK if nothing is recorded.
  */
@@ -400,13 +401,18 @@ KDA_API kda_status kda_chunk_prefill_host(const void *q, const void *k, const vo
  *    reciprocal is formed.  A token of -100 or below, -infinity among them,
  *    forgets all before it: its decay, and that over any tokens whose g sum to
  *    -100 or below, is exactly 0 (exp(-100) is 3.7e-44).  Values above 0 are outside the contract (fp32 uses them as
- *    given; bf16 results are unspecified).  KDA_DEBUG_CHECKS scans nothing here.
+ *    given; bf16 results are unspecified).
  *  - Keys need not be unit vectors (their scale is taken out per row), but bf16
- *    wants 0 <= beta |k|^2 <= 2, where no token's step enlarges the state, and
- *    beta_r |k_r| |k_s| and beta_s |k_r| |k_s| below 2^15 for any two tokens r, s
- *    of a chunk of 32: then (I + A)^-1, which has no larger element, fits fp16.
- *    The bf16 backward also wants beta <= 4.  Beyond these the bf16 results are
- *    unspecified (possibly not finite); fp32 has no such limit.
+ *    prefill and backward want 0 <= beta |k|^2 <= 2, where no token's step enlarges
+ *    the state (1/32 more is taken: unit keys and beta round to bf16), and
+ *    beta_r |k_r| |k_s| and beta_s |k_r| |k_s| below 2^14 for any two tokens r, s
+ *    of a chunk of 32: then (I + A)^-1, whose elements are below 2.6 times that,
+ *    fits fp16.  The bf16 backward also wants beta <= 4.  Beyond these the bf16
+ *    results are unspecified (possibly not finite); fp32 and decode have no such
+ *    limit.
+ *  - KDA_DEBUG_CHECKS=1 scans the rows of the sequences (in decode the tokens that
+ *    are taken) for g above 0 or NaN and, in the bf16 prefill and backward, for keys
+ *    and beta beyond these limits: KDA_ERR_INPUT_RANGE.
  *  - q, k, v, o and the states must be 16-byte aligned (KDA_ERR_INVALID_ARG).
  *  - rows < 2^31 - 64 and N H < 2^28, else KDA_ERR_UNSUPPORTED.
  *  - A non-finite input makes the results of its own (sequence, head) unspecified,

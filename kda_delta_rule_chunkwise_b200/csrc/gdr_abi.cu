@@ -14,6 +14,12 @@ bool head_dim(int d) { return d == 64 || d == 128; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 kda_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
+// The debug input scan ahead of a call, if it is switched on.
+kda_status scan_inputs(const kda::GdrScanArgs &a, kda_dtype dtype, cudaStream_t st) {
+    if (!kda::debug_checks_enabled()) return KDA_OK;
+    return from_cuda(kda::launch_gdr_scan(a, dtype == KDA_BF16, st));
+}
+
 // Checks shared by the calls over sequences; KDA_OK if they hold.
 kda_status check_sequences(bool packed, int B, int64_t T, int N, int Hk, int H, int dk, int dv,
                            kda_dtype dtype) {
@@ -71,6 +77,9 @@ kda_status kda_gdr_chunk_prefill(const void *q, const void *k, const void *v, co
     uint32_t *err = kda::device_error_word();
     if (!err) return KDA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const kda_status scanned = scan_inputs(
+        {k, g, beta, cu_seqlens, nullptr, T, N, Hk, H, dk, dtype == KDA_BF16, false, err}, dtype, st);
+    if (scanned != KDA_OK) return scanned;
     kda::Profiler::begin(st);
     if (dtype == KDA_BF16) {
         const kda::GdrArgs a{q, k, v, g, beta, state_in, cu_seqlens, T, B * T, N, Hk, H, dk, dv,
@@ -97,6 +106,9 @@ kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const voi
     uint32_t *err = kda::device_error_word();
     if (!err) return KDA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const kda_status scanned =
+        scan_inputs({k, g, beta, nullptr, lens, L, N, Hk, H, dk, false, false, err}, dtype, st);
+    if (scanned != KDA_OK) return scanned;
     kda::Profiler::begin(st);
     const kda::GdrTokenArgs a{q, k, v, g, beta, state, update_state ? state : nullptr, nullptr,
                               slots, lens, L, N, P, Hk, H, dk, dv, o, err};
@@ -134,6 +146,9 @@ kda_status kda_gdr_backward(const void *q, const void *k, const void *v, const v
     uint32_t *err = kda::device_error_word();
     if (!err) return KDA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const kda_status scanned = scan_inputs({k, g, beta, cu_seqlens, nullptr, T, N, Hk, H, dk, dtype == KDA_BF16,
+                                            dtype == KDA_BF16, err}, dtype, st);
+    if (scanned != KDA_OK) return scanned;
     kda::Profiler::begin(st);
     const kda::GdrArgs a{q, k, v, g, beta, state_in, cu_seqlens, T, B * T, N, Hk, H, dk, dv,
                          nullptr, nullptr, err, kda::next_launch_epoch()};

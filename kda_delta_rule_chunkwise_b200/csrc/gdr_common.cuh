@@ -14,6 +14,8 @@ namespace gdr {
 
 constexpr int kChunk = 32;          // tokens per chunk of the chained kernels
 constexpr float kMinLogDecay = -100.f;
+// Limits of the bf16 calls (kda.h): beta |k|^2, beta |k_r| |k_s| in a chunk, beta in the backward.
+constexpr float kMaxStep = 2.f + 1.f / 32, kMaxCross = 16384.f, kMaxBeta = 4.f;
 // A log-decay, -infinity among them, as the kernels sum it: not below the clamp.  A NaN stays one.
 __device__ __forceinline__ float log_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }
 // exp of a log-decay or a sum of them, exactly 0 from the clamp down: a token that forgets leaves nothing

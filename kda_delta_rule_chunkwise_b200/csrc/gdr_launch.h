@@ -52,6 +52,18 @@ cudaError_t launch_gdr_recompute(const GdrArgs &a, const GdrImages &m, const Gdr
 cudaError_t launch_gdr_backward(const GdrArgs &a, const GdrGrads &g, int64_t rows, bool bf16,
                                 void *workspace, cudaStream_t st);
 
+// The debug input scan (gdr_debug.cu): g above 0 or NaN; `chunked`: the limits of the bf16 calls on the
+// chunks as well, `backward`: and on beta.
+struct GdrScanArgs {
+    const void *k, *g, *beta;
+    const int32_t *cu_seqlens, *lens;   // either may be nullptr
+    int64_t T;
+    int N, Hk, H, dk;
+    bool chunked, backward;
+    uint32_t *err;
+};
+cudaError_t launch_gdr_scan(const GdrScanArgs &a, bool bf16, cudaStream_t st);
+
 // Token by token in fp32 arithmetic (gdr_token.cu): the decode step for either type, and the
 // fp32 prefill.  State entries are slots[n] of P where given.
 struct GdrTokenArgs {

@@ -421,3 +421,58 @@ def test_a_nan_decay_shows_in_its_sequence_and_head(dtype):
     o = binding.kda_gdr_decode(*d, state)
     assert torch.isnan(o[0, 1:, 1]).all() and torch.isnan(state[0, 1]).all()
     assert torch.isfinite(o[0, :, [0, 2]]).all() and torch.isfinite(state[0, [0, 2]]).all() and torch.isfinite(o[0, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_the_debug_scan_reports_inputs_outside_the_contract(monkeypatch, dtype):
+    """Positive and NaN decays in any call; keys and beta beyond the bf16 limits where they hold."""
+    while binding.kda_check_device_error() != binding.KDA_OK:
+        pass
+    base = gpu(ref.inputs(1, 100, 2, 4, 128, 128, dtype, seed=51, lengths=[30, 0, 60]))
+    dout = torch.randn(1, 100, 4, 128, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    want = binding.kda_gdr_chunk_prefill(*base)
+    want_back = binding.kda_gdr_backward(*base, dout)
+    monkeypatch.setenv("KDA_DEBUG_CHECKS", "1")
+
+    def reports(which, value, at, back=False):
+        x = [None if t is None else t.clone() for t in base]
+        x[which][at] = value
+        binding.kda_gdr_backward(*x, dout) if back else binding.kda_gdr_chunk_prefill(*x)
+        code = binding.kda_check_device_error()
+        assert code in (binding.KDA_OK, binding.KDA_ERR_INPUT_RANGE)
+        assert binding.kda_check_device_error() == binding.KDA_OK
+        return code == binding.KDA_ERR_INPUT_RANGE
+
+    got, back = binding.kda_gdr_chunk_prefill(*base), binding.kda_gdr_backward(*base, dout)
+    assert binding.kda_check_device_error() == binding.KDA_OK
+    assert torch.equal(got[0][:, :90], want[0][:, :90]) and torch.equal(got[1], want[1])      # nothing changes
+    assert all(torch.equal(a, b) for a, b in zip(back, want_back))
+    for back in (False, True):
+        for bad in (1e-3, float("nan"), math.inf):
+            assert reports(3, bad, (0, 89, 3), back) and not reports(3, bad, (0, 90, 3), back)   # 90: of no sequence
+        assert not reports(3, -math.inf, (0, 5, 0), back)
+        # a unit key times 1.42 is |k|^2 = 2.02, times 1.5 2.25; beta = 1
+        one = lambda f: base[1][0, 40, 1] / base[1][0, 40, 1].float().norm().to(dtype) * f
+        base[4][0, 40] = 1.0
+        assert not reports(1, one(1.4), (0, 40, 1), back) and reports(1, one(1.5), (0, 40, 1), back) == (dtype == BF)
+        assert reports(4, -0.1, (0, 40, 2), back) == (dtype == BF)
+        # beta_r |k_r| |k_s| = 2^-16 2^8 2^23: each beta |k|^2 is at most 1, their cross term 2^15
+        x = [None if t is None else t.clone() for t in base]
+        for row, size, b in ((30, 2.0 ** 8, 2.0 ** -16), (31, 2.0 ** 23, 2.0 ** -46)):
+            x[1][0, row] = 0
+            x[1][0, row, :, 0], x[4][0, row] = size, b
+        binding.kda_gdr_chunk_prefill(*x)
+        assert (binding.kda_check_device_error() == binding.KDA_ERR_INPUT_RANGE) == (dtype == BF)
+    x = [None if t is None else t.clone() for t in base]
+    x[1][0, 40], x[4][0, 40] = x[1][0, 40] * 0.1, 5.0
+    binding.kda_gdr_chunk_prefill(*x)
+    assert binding.kda_check_device_error() == binding.KDA_OK
+    binding.kda_gdr_backward(*x, dout)
+    assert (binding.kda_check_device_error() == binding.KDA_ERR_INPUT_RANGE) == (dtype == BF)
+
+    d = [t[:, :8].reshape(2, 4, *t.shape[2:]).contiguous() for t in base[:5]]
+    state = torch.zeros(2, 4, 128, 128, device="cuda")
+    d[3][1, 2, 3] = 0.5
+    for lens, code in ((None, binding.KDA_ERR_INPUT_RANGE), ([4, 3], binding.KDA_ERR_INPUT_RANGE), ([4, 2], binding.KDA_OK)):
+        binding.kda_gdr_decode(*d, state, lens=None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda())
+        assert binding.kda_check_device_error() == code
