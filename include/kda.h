@@ -414,7 +414,7 @@ KDA_API kda_status kda_chunk_prefill_host(const void *q, const void *k, const vo
  *    are taken) for g above 0 or NaN and, in the bf16 prefill and backward, for keys
  *    and beta beyond these limits: KDA_ERR_INPUT_RANGE.
  *  - q, k, v, o and the states must be 16-byte aligned (KDA_ERR_INVALID_ARG).
- *  - rows < 2^31 - 64 and N H < 2^28, else KDA_ERR_UNSUPPORTED.
+ *  - rows < 2^31 - 64, N H < 2^28 and rows H <= 2^40, else KDA_ERR_UNSUPPORTED.
  *  - A non-finite input makes the results of its own (sequence, head) unspecified,
  *    tokens before it in the same 32-token chunk among them (in the backward any tokens
  *    before it, and dq and dk of its key head); no other unit's.  A NaN in g shows in them.

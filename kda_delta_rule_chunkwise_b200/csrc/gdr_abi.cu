@@ -20,6 +20,11 @@ kda_status scan_inputs(const kda::GdrScanArgs &a, kda_dtype dtype, cudaStream_t 
     return from_cuda(kda::launch_gdr_scan(a, dtype == KDA_BF16, st));
 }
 
+// Sizes that the kernels' indexes and the workspaces' byte counts hold.
+bool sizes_held(int64_t rows, int N, int H) {
+    return rows <= INT32_MAX - 64 && (int64_t)N * H <= INT32_MAX / 8 && rows * H <= (int64_t)1 << 40;
+}
+
 // Checks shared by the calls over sequences; KDA_OK if they hold.
 kda_status check_sequences(bool packed, int B, int64_t T, int N, int Hk, int H, int dk, int dv,
                            kda_dtype dtype) {
@@ -29,8 +34,7 @@ kda_status check_sequences(bool packed, int B, int64_t T, int N, int Hk, int H, 
     if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
     if (packed ? B != 1 : N != B) return KDA_ERR_INVALID_ARG;
     if (!head_dim(dk) || !head_dim(dv)) return KDA_ERR_UNSUPPORTED;
-    if ((int64_t)N * H > INT32_MAX / 8) return KDA_ERR_UNSUPPORTED;
-    if (T > INT32_MAX - 64 || (B > 0 && T > (INT32_MAX - 64) / B)) return KDA_ERR_UNSUPPORTED;
+    if (T > INT32_MAX - 64 || !sizes_held(B * T, N, H)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -52,7 +56,8 @@ extern "C" {
 
 size_t kda_gdr_prefill_workspace_bytes(int64_t rows, int N, int Hk, int H, int dk, int dv,
                                        kda_dtype dtype) {
-    if (rows < 0 || N <= 0 || Hk <= 0 || H <= 0 || H % Hk != 0 || !head_dim(dk) || !head_dim(dv))
+    if (rows < 0 || N <= 0 || Hk <= 0 || H <= 0 || H % Hk != 0 || !head_dim(dk) || !head_dim(dv) ||
+        !sizes_held(rows, N, H))
         return 0;
     return dtype == KDA_BF16 ? kda::gdr_image_bytes(rows, N, Hk, H, dk, false) : 0;
 }
@@ -117,7 +122,8 @@ kda_status kda_gdr_decode(const void *q, const void *k, const void *v, const voi
 
 size_t kda_gdr_backward_workspace_bytes(int64_t rows, int N, int Hk, int H, int dk, int dv,
                                         kda_dtype dtype) {
-    if (rows < 0 || N < 0 || Hk <= 0 || H <= 0 || H % Hk != 0 || !head_dim(dk) || !head_dim(dv))
+    if (rows < 0 || N < 0 || Hk <= 0 || H <= 0 || H % Hk != 0 || !head_dim(dk) || !head_dim(dv) ||
+        !sizes_held(rows, N, H))
         return 0;
     return kda::gdr_backward_workspace_bytes(rows, N, Hk, H, dk, dv, dtype == KDA_BF16);
 }

@@ -162,3 +162,12 @@ def test_second_derivatives_are_refused_not_dropped(monkeypatch):
     a, b = binding.kda_block_norm_autograd(x, y, None, w, w)
     (a.sum() + b.sum()).backward()
     assert torch.equal(x.grad, 2 * x) and not x.grad.requires_grad
+
+
+def test_sizes_whose_workspace_no_number_holds_are_refused(lib):
+    """2^26 chunks of 2^27 heads are more bytes than 64 bits count: a wrapped sum would take any workspace."""
+    huge = dict(T=2 ** 31 - 128, Hk=1, H=2 ** 27, workspace_bytes=2 ** 63)
+    assert prefill(lib, **huge) == NOT and backward(lib, **huge) == NOT
+    for f in (lib.kda_gdr_prefill_workspace_bytes, lib.kda_gdr_backward_workspace_bytes):
+        assert f(2 ** 31 - 128, 1, 1, 2 ** 27, 128, 128, binding.KDA_BF16) == 0
+        assert f(2 ** 31 - 128, 1, 1, 2 ** 9, 128, 128, binding.KDA_BF16) > 2 ** 40
