@@ -306,3 +306,31 @@ def test_backward_of_a_nan_decay_shows_it(dtype):
     assert torch.equal(got[5][0], clean[5][0]) and torch.equal(got[5][1, keep], clean[5][1, keep])
     for i in (0, 1):                               # key head 1 has value heads 2 and 3
         assert torch.equal(got[i][0, :50], clean[i][0, :50]) and torch.equal(got[i][0, :, 1], clean[i][0, :, 1])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("g", [-60.0, -math.inf])
+def test_state_gradient_through_strong_decay(g, dtype):
+    """What reaches the state before 90 tokens: a share of exp(-60) of the first token's, or nothing."""
+    x, dout, ds = case(1, 90, 1, 2, 128, 128, dtype, 8, g=g)
+    want = ref.backward(*x[:5], x[5], None, dout, ds)[5]
+    got = binding.kda_gdr_backward(*gpu(x[:6]), None, dout.cuda(), ds.cuda())[5]
+    assert off(got, want) <= bar(F32, 90) and float(got.abs().max()) <= 1e-20
+
+
+@pytest.mark.parametrize("shape", [(1, 300, 2, 4, 128, 128), (2, 130, 1, 2, 64, 128), (1, 200, 2, 2, 128, 64)],
+                         ids=lambda c: "x".join(map(str, c)))
+@pytest.mark.parametrize("dout_size,ds_size,g", [(1.0, 0.3, None), (2.0 ** -10, 1.0, -0.01), (1.0, 0.0, None), (0.0, 1.0, -0.01)])
+def test_bf16_gradients_are_off_by_their_rounding(shape, dout_size, ds_size, g):
+    """A bar for sums of many independent roundings, also where dg is the state's share alone (little or no dout,
+    slow decay).  A rounding to bf16 is uniform in half a step, 2^-8 of a value at most: its RMS is 2^-8 / sqrt 3 at
+    most.  The six products of a gradient have two operands each with fp16 roundings of RMS 2^-11 / sqrt 3, and may
+    cancel by a factor of two: sqrt(12) x 2 x 2^-11 / sqrt 3.  Together sqrt(2^-16 / 3 + 48 x 2^-22 / 3) = 3.0e-3."""
+    B, T, Hk, H, dk, dv = shape
+    x, dout, ds = case(B, T, Hk, H, dk, dv, BF, T + 1, **({} if g is None else dict(g=g)))
+    dout, ds = dout * dout_size, ds * ds_size
+    want = ref.backward(*x[:5], x[5], None, dout, ds)
+    got = binding.kda_gdr_backward(*gpu(x[:6]), None, dout.cuda(), ds.cuda())
+    for name, a, b in zip(NAMES, got, want):
+        limit = bar(F32, T) if name == "dstate_in" else math.sqrt(2.0 ** -16 / 3 + 48 * 2.0 ** -22 / 3)
+        assert off(a, b) <= limit, (name, off(a, b))
