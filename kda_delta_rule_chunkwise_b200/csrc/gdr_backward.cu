@@ -166,7 +166,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32)
 #pragma unroll
             for (int t = 0; t < 4; ++t) mine[t * 32] = make_float4(y[t][0], y[t][1], y[t][2], y[t][3]);
             __syncwarp();
-            if (lane == 0) mbar_arrive(pipe.swapped + (group * 2 + (part ^ 1)) * 2 + (it & 1));
+            if (lane == 0) mbar_arrive(pipe.swapped + group);
             if (it > 0) write_dv(row + kChunk, valid - kChunk);   // the chunk after this one
         }
         // What does not depend on the other half, while its sums are on their way: dO^T in the scaled
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, true, true, 0>::WARPS * 32)
             }
         }
         if (KS == 2) {
-            ok = pipe.wait(pipe.swapped + (group * 2 + part) * 2 + (it & 1), (it >> 1) & 1);
+            ok = pipe.wait(pipe.swapped + group, it & 1);
             if (!ok) break;
             const float4 *other = reinterpret_cast<const float4 *>(smem + M::SWAP) +
                                   (((group * 2 + (it & 1)) * 2 + (part ^ 1)) * XF / 4) * 32 + lane;

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
 #pragma unroll
             for (int t = 0; t < 4; ++t) mine[t * 32] = make_float4(y[t][0], y[t][1], y[t][2], y[t][3]);
             __syncwarp();
-            if (lane == 0) mbar_arrive(pipe.swapped + (group * 2 + (part ^ 1)) * 2 + (ci & 1));
+            if (lane == 0) mbar_arrive(pipe.swapped + group);
         }
         // what does not depend on the other half, while it is on its way: this half's Q S, for the output
         // warp, and the operands of what follows
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__((Pipe<DK, NCW, KS, false, !REC, hand_bytes<KS,
             ldsm4(xl[2], at + L::XL + 16 * L::XP + 32);
         }
         if (KS == 2) {
-            ok = pipe.wait(pipe.swapped + (group * 2 + part) * 2 + (ci & 1), (ci >> 1) & 1);
+            ok = pipe.wait(pipe.swapped + group, ci & 1);
             if (!ok) break;
             const float4 *other = reinterpret_cast<const float4 *>(smem + M::SWAP) +
                                   (((group * 2 + (ci & 1)) * 2 + (part ^ 1)) * 4) * 32 + lane;

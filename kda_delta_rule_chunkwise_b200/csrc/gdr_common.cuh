@@ -310,14 +310,14 @@ struct Pipe {
     static constexpr int SWAP = OUT + CHAIN * kChunk * OP;
     static constexpr int HAND = SWAP + (KS == 2 ? NCW * 2 * 2 * 16 * 32 * 4 : 0);
     static constexpr int BARS = HAND + OW * ST * OUTW;
-    static constexpr int BYTES = BARS + (2 * ST + 4 * NCW + OW * ST) * 8 + 16;
+    static constexpr int BYTES = BARS + (2 * ST + NCW + OW * ST) * 8 + 16;
     static_assert(BYTES <= 227 * 1024, "shared memory of a CTA");
 
     unsigned char *smem;
-    // swapped: KS = 2's exchange, two barriers per warp that alternate like the buffers.  The other warp's
-    // arrival for chunk c + 2 waits for this warp's for c + 1, which follows this warp's wait for c: no
-    // barrier is ever more than one phase ahead of its wait.  (With one barrier per warp the other's
-    // arrival for c + 1 could come before this warp's wait for c, whose parity then names a phase to come.)
+    // swapped: KS = 2's exchange, one barrier per group at which both warps arrive and wait.  Its phase
+    // c + 1 needs both warps' arrivals for c + 1, and each follows that warp's wait for c: no phase ends
+    // before the one before it has been waited for.  (A barrier at which only the other warp arrives could
+    // be a phase further on when this one comes to wait, whose parity then names a phase to come.)
     uint64_t *full, *empty, *swapped, *handed;
     volatile uint32_t *abort;
     uint32_t *err;
@@ -325,14 +325,14 @@ struct Pipe {
 
     __device__ __forceinline__ Pipe(unsigned char *s, uint32_t *e, uint32_t ep) : smem(s), err(e), epoch(ep) {
         full = reinterpret_cast<uint64_t *>(smem + BARS);
-        empty = full + ST, swapped = empty + ST, handed = swapped + 4 * NCW;
+        empty = full + ST, swapped = empty + ST, handed = swapped + NCW;
         abort = reinterpret_cast<volatile uint32_t *>(handed + OW * ST);
         if (threadIdx.x == 0) {
             for (int i = 0; i < ST; ++i) {
                 mbar_init(full + i, 1);
                 mbar_init(empty + i, CHAIN + OW);
             }
-            for (int i = 0; i < 4 * NCW; ++i) mbar_init(swapped + i, 1);
+            for (int i = 0; i < NCW; ++i) mbar_init(swapped + i, KS);
             for (int i = 0; i < OW * ST; ++i) mbar_init(handed + i, KS);
             mbar_fence_init();
             *abort = 0u;

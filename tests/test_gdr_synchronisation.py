@@ -57,50 +57,50 @@ def test_no_buffer_of_the_decode_kernel_is_read_and_written_between_two_barriers
 
 
 def test_two_warps_of_a_column_group_never_miss_each_other():
-    """Each warp hands its half sums over, arrives at the other's barrier and waits at its own, chunk after
-    chunk.  A wait asks for a parity, so a warp that is late by two phases would wait for ever: no order of
+    """Each warp hands its half sums over, arrives at a barrier and waits at one, chunk after chunk.  A wait
+    asks for a parity, so a warp that is late by two phases would wait for ever: no order of
     the two warps' steps may come to a halt, or let a warp read a buffer too early or too late."""
     pipe = source("gdr_common.cuh")
-    barriers = int(re.search(r"i < (\d+) \* NCW; \+\+i\) mbar_init\(swapped \+ i, 1\)", pipe).group(1))
-    assert f"(2 * ST + {barriers} * NCW + OW * ST) * 8" in pipe         # their place in shared memory
-    assert f"handed = swapped + {barriers} * NCW" in pipe
+    groups = 2
+    number, arrivals = re.search(r"i < (.*); \+\+i\) mbar_init\(swapped \+ i, (.*)\);", pipe).groups()
+    assert f"(2 * ST + {number} + OW * ST) * 8" in pipe and f"handed = swapped + {number};" in pipe   # their place
+    number, arrivals = (eval(e, {"NCW": groups, "KS": 2}) for e in (number, arrivals))
     for name, step in (("gdr_chunk.cu", "ci"), ("gdr_backward.cu", "it")):
         text = source(name)
         (arrive,) = re.findall(r"mbar_arrive\(pipe\.swapped \+ (.*)\);", text)
         (index, parity), = re.findall(r"pipe\.wait\(pipe\.swapped \+ (.*), ([^,\n]*)\);\n", text)
         chunks = 7
 
-        def value(expr, part, chunk):
-            return eval(expr, {"group": 0, "part": part, step: chunk})   # C and Python agree on these operators
+        def value(expr, part, chunk, group=0):
+            return eval(expr, {"group": group, "part": part, step: chunk})   # C and Python agree on these operators
 
-        for part in range(2):
-            for c in range(chunks):
-                assert 0 <= value(index, part, c) < barriers
-                assert value(arrive, part, c) == value(index, part ^ 1, c)
+        used = [{value(e, part, c, g) for e in (arrive, index) for part in range(2) for c in range(chunks)}
+                for g in range(groups)]
+        assert not used[0] & used[1] and all(0 <= i < number for u in used for i in u)
         # a warp's steps: 4 c write its half of buffer c & 1; 4 c + 1 arrive; 4 c + 2 wait; 4 c + 3 read the other's
-        todo, known = [((0, 0), (0,) * barriers)], set()
+        todo, known = [((0, 0), (0,) * number)], set()
         while todo:
             state = todo.pop()
             if state in known:
                 continue
             known.add(state)
-            at, phases = state
+            at, arrived = state
             moved = False
             for part in range(2):
                 c, what = divmod(at[part], 4)
                 if c == chunks:
                     continue
-                after = list(phases)
+                after = list(arrived)
                 if what == 1:
                     after[value(arrive, part, c)] += 1
-                elif what == 2 and phases[value(index, part, c)] & 1 == value(parity, part, c):
+                elif what == 2 and arrived[value(index, part, c)] // arrivals & 1 == value(parity, part, c):
                     continue   # the phase asked for is the one in progress
                 elif what == 3:
                     other = at[part ^ 1]
                     assert 4 * c + 1 < other <= 4 * (c + 2), (name, "read at the wrong time", at)
                 moved = True
                 todo.append((tuple(a + (i == part) for i, a in enumerate(at)), tuple(after)))
-            assert moved or at == (4 * chunks, 4 * chunks), (name, "both warps wait", at, phases)
+            assert moved or at == (4 * chunks, 4 * chunks), (name, "both warps wait", at, arrived)
 
 
 def test_no_wait_that_gives_up_leaves_copies_behind():
