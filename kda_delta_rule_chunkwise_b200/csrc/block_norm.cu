@@ -4,10 +4,14 @@
 //     x' = x + scale sigmoid(gate) n               gate, scaled residual sum
 //     h  = x' rsqrt(mean x'^2 + eps) w_pre         norm before the next block
 //
-// Every input is read once and every output written once, a row's values stay in registers
-// between the row sums.  All arithmetic is fp32; h is taken from the unrounded x'.  8192 rows of
-// 4096, bf16: forward 62 us for 336 MB (5.4 TB/s, 84 % of a plain copy); backward 133 us for
-// 537 MB (62 %), bound by instruction issue and the latency of its three row sums.
+// Every input is read once and every output written once.  All arithmetic is fp32; h is taken from
+// the unrounded x'.  Up to a width of 4096 a row's values stay in registers between the row sums; 8192
+// rows of 4096, bf16: forward 63 us for 336 MB (5.3 TB/s, 82 % of a plain copy); backward 133 us for
+// 537 MB (62 %), bound by the latency of its three row sums and by instruction issue (51 % of cycles).
+// Wider rows, several vectors to a thread, do not all fit: the backward spills about 300 bytes a thread
+// up to 8192 and 1.1 KB beyond, the forward some beyond 8192 (8192 rows of 5120 and of 8192, bf16: forward
+// 100 and 106 us, 65 and 98 % of a plain copy's speed; backward 331 and 367 us, 31 and 45 %; 4096 rows of
+// 16384: 135 us, 77 %, and 930 us, 18 %).
 //
 // Backward, with r_y, r_x the two rsqrt factors, a = sigmoid(gate), D the width:
 //     gx = dh w_pre;   dx = dx' + r_x (gx - x' r_x^2 sum(gx x') / D)

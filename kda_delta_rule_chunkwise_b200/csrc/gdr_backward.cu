@@ -27,8 +27,8 @@
 // kernel's products take fp16 operands scaled by a power of two per tile (2^-11 each, 29 binary
 // orders below the tile's largest value), below the rounding of its bf16 outputs.
 //
-// At 8192 tokens of 32 heads (dk = dv = 128): chunks 70 us, the forward's chain 363, the adjoint's
-// 477 (latency of a chunk's steps, like the forward's), the blocks' gradients 408 (shared-memory reads
+// At 8192 tokens of 32 heads (dk = dv = 128): chunks 70 us, the forward's chain 360, the adjoint's
+// 479 (latency of a chunk's steps, like the forward's), the blocks' gradients 401 (shared-memory reads
 // of the operands and the loads between barriers); the operator's bytes would take 53 us.
 #include "gdr_common.cuh"
 #include "gdr_launch.h"

@@ -25,8 +25,8 @@
 // only o depends on (S and beta N in its two products, P) is rounded once to fp16, 2^-12,
 // below o's own rounding to bf16.
 //
-// What bounds it: with few heads the latency of a chunk's dependent steps, 2600 cycles of which the
-// matrix instructions are 800 (350 us for 8192 tokens of 32 heads, dk = dv = 128, beside 60 us for
+// What bounds it: with few heads the latency of a chunk's dependent steps, 2500 cycles of which the
+// matrix instructions are 800 (354 us for 8192 tokens of 32 heads, dk = dv = 128, beside 55 us for
 // the chunks; the operator's bytes would take 32 us); with many the matrix pipe and the shared memory
 // that feeds it, each half busy with the two warps per SM quarter that the registers allow (641 us
 // for 16 packed prompts of 30011 tokens together; the operator's bytes would take 106 us).

@@ -408,7 +408,9 @@ inline cudaError_t launch_chain_kernel(void (*kernel)(const CUtensorMap, const A
 // (148 units).  So 32 and 48 heads take 179 against 215 and 377 us, and 349 against 216 and 377; 96
 // heads 520 against 420 and 378; 160 heads 862 against 626 and 740.  The choice is the least of rounds
 // times that; packed sequences, which are ragged, fill the rounds' ends, so there their number is not
-// rounded up.
+// rounded up.  The same numbers serve the adjoint, whose rounds take 243, 353 and 640 us, and d = 64 (154
+// us a round of 32 or 64 columns): their least is the same variant at 16, 32, 37, 48, 74, 96, 148 and 160
+// heads.
 inline int chain_variant(int64_t units, int dv, bool packed) {
     struct { int columns, variant; double us; } const all[3] = {{32, 22, 179.}, {64, 41, 216.}, {128, 81, 377.}};
     int best = 0;

@@ -9,8 +9,8 @@
 // One decode token is bound by HBM: each state (dk x dv fp32, 64 KiB at d = 128) is read
 // and written once, everything else is about 1 KiB.  With L tokens the state stays in
 // registers between them, so they cost one pass over it as well.  256 requests of 32 heads:
-// 183 us for 1.08 GB (5.9 TB/s, 91 % of a plain copy); 48 requests of up to 5 tokens: 45 us
-// for 204 MB, the tokens' barriers beside the pass.
+// 185 us for 1.08 GB (5.9 TB/s, 90 % of a plain copy); 48 requests of up to 5 tokens: 49 us
+// for 204 MB, the tokens' barriers beside the pass.  Without the update: 103 us for 256 tokens.
 //
 // One CTA of 256 threads per (n, h, slice of DVS columns).  A thread keeps a
 // (DK / RG) x 4 block of S in registers, loaded as coalesced 16-byte vectors.  The sums
@@ -271,9 +271,9 @@ static cudaError_t launch_token_t(const GdrTokenArgs &a, cudaStream_t st) {
 
 template <int DK, typename Tin>
 static cudaError_t launch_token_d(const GdrTokenArgs &a, cudaStream_t st) {
-    // few (request, head) units: narrow slices, so that more SMs read the states (32 heads of 128: 1
-    // request 9.9 us against 11.7 with whole states, 2 requests 10.0 against 10.7, 4 the same, 8
-    // requests 13.2 against 12.1)
+    // few (request, head) units: narrow slices, so that more SMs read the states (32 heads of 128, times
+    // between events around the launch: 1 request 9.9 us against 11.7 with whole states, 2 requests 10.0
+    // against 10.7, 4 the same, 8 requests 13.2 against 12.1)
     const int64_t units = (int64_t)a.N * a.H;
     if (units * (a.dv / 32) <= 2 * 148) return launch_token_t<DK, 32, Tin>(a, st);
     return a.dv == 64 ? launch_token_t<DK, 64, Tin>(a, st) : launch_token_t<DK, 128, Tin>(a, st);
