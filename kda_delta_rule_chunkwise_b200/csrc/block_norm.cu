@@ -120,11 +120,28 @@ __device__ __forceinline__ float2 row_sum2(float x, float y, float2 *red) {
     return make_float2(x, y);
 }
 
+constexpr double kLog2eExact = 1.44269504088896340736;
+constexpr float kLog2e = (float)kLog2eExact, kLog2eLow = (float)(kLog2eExact - (double)kLog2e);
+
 // r^2 mean of a norm's gradient r (z - u r^2 mean(z u)), factor by factor: r mean is of z's size, while r^2
 // and r^3 alone leave the range of fp32 beside a small eps or with large rows (a row of zeros would be 0 inf).
 __device__ __forceinline__ float mean_term(float mean, float r) { return mean * r * r; }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// The gate of logits of type T.  Beside bf16 values the fast exponential, whose error of 2^-24 |x| and two
+// steps is far below a rounding to bf16.  fp32 gets 2^(-x log2 e) with the product's rounding error recovered by
+// a fused multiply-add (Dekker's exact product) and log2 e in two terms: a few steps of 2^-24 for any x; and the
+// fast quotient (two steps).  8192 x 4096 in fp32: forward 119 us, backward 217; with the fast exponential 112
+// and 207, with expf and a rounded quotient 127 and 231.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float x) {
+    if constexpr (sizeof(T) == 2) return __fdividef(1.f, 1.f + __expf(-x));
+    asm("max.NaN.f32 %0, %0, 0fC3160000;" : "+f"(x));   // to [-150, 150], where nothing is left to tell;
+    asm("min.NaN.f32 %0, %0, 0f43160000;" : "+f"(x));   // a NaN stays
+    const float t = x * -kLog2e, low = fmaf(x, -kLog2eLow, fmaf(x, -kLog2e, -t));
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return __fdividef(1.f, 1.f + e * fmaf(low, 0.6931471805599453f, 1.f));
+}
 
 
 // The inputs of the rows that a CTA works on: NT / TPR rows side by side, TPR threads and NV
@@ -296,7 +313,7 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_kernel(BlockNormArgs a) {
             const int c = (i * TPR + t) * V;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float s = gated ? sigmoid(in.g[i].get(j)) : 1.f;
+                const float s = gated ? sigmoid<T>(in.g[i].get(j)) : 1.f;
                 xn[i][j] = fmaf(in.y[i].get(j) * ry * wo[i].get(j), s, in.x[i].get(j));
                 ss = fmaf(xn[i][j], xn[i][j], ss);
             }
@@ -383,7 +400,7 @@ __global__ void __launch_bounds__(NT, CTAS) block_norm_backward_kernel(BlockNorm
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                s[i][j] = gated ? sigmoid(in.g[i].get(j)) : 1.f;
+                s[i][j] = gated ? sigmoid<T>(in.g[i].get(j)) : 1.f;
                 xn[i][j] = fmaf(in.y[i].get(j) * ry * wo[i].get(j), a.scale * s[i][j], in.x[i].get(j));
                 sx = fmaf(xn[i][j], xn[i][j], sx);
                 sg = fmaf(in.dh[i].get(j) * wi[i].get(j), xn[i][j], sg);
@@ -494,7 +511,7 @@ __global__ void __launch_bounds__(kAnyThreads) block_norm_any_kernel(BlockNormAr
             if (BACK && dxn) fetch<V>(d, dxn + c);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                s[j] = gate ? sigmoid(s[j]) : 1.f;
+                s[j] = gate ? sigmoid<T>(s[j]) : 1.f;
                 if (!(BACK && dh)) h[j] = 0.f;
                 if (!(BACK && dxn)) d[j] = 0.f;
             }

@@ -251,3 +251,24 @@ def test_second_derivatives_are_refused_not_dropped():
     assert all(torch.equal(p, q) for p, q in zip(grads, plain))
     with pytest.raises(RuntimeError, match="second derivative"):
         (a.sum() + grads[1].square().sum()).backward()
+
+
+@pytest.mark.parametrize("D", [64, 66, 65])
+def test_gates_in_fp32_are_fp32s(D):
+    """Logits from -80 to 80, each value alone: the gate's own digits show in x' where x is 0 and in dgate.  Steps of
+    2^-24 at most: the row sum D / 32 + 8 and half of it in the factor, its square root 2, the exponential 4 (two
+    units), the gate's sum and quotient 4, four products; in dgate the gate twice and 1 - a, which is off by 2^-24 / (1 - a)
+    where a is near 1: compare it there as an absolute share."""
+    x, y, _, wo, wi, dxn, _ = make(161, D, F32, F32, True, seed=D, y_std=1.0)
+    g = torch.linspace(-80, 80, 161)[:, None].expand(161, D).contiguous()
+    x = torch.zeros_like(x)
+    got = binding.kda_block_norm(*cuda([x, y, g, wo, wi]))[0].cpu().double()
+    want = formulas(*(t.double() for t in (x, y, g, wo, wi)), 1.0, 1e-6)[0]
+    assert float(((got - want) / want).abs().max()) <= 2.0 ** -24 * (D / 64 + 4 + 2 + 4 + 4 + 4)
+    leaves = [t.double().requires_grad_(True) for t in (x, y, g, wo, wi)]
+    want = torch.autograd.grad(formulas(*leaves, 1.0, 1e-6)[0], leaves[2], dxn.double())[0]
+    got = binding.kda_block_norm_backward(*cuda([x, y, g, wo, wi]), dxn.cuda(), None)[2].cpu().double()
+    n = formulas(*(t.double() for t in (x, y)), None, wo.double(), wi.double(), 1.0, 1e-6)[0]
+    a = torch.sigmoid(g.double())
+    steps = 2.0 ** -24 * (D / 64 + 4 + 2 + 2 * (4 + 4) + 6)
+    assert ((got - want).abs() <= steps * want.abs() + 2.0 ** -24 * 2 * (dxn.double() * n * a).abs()).all()
