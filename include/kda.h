@@ -400,8 +400,8 @@ KDA_API kda_status kda_chunk_prefill_host(const void *q, const void *k, const vo
  *  - g has no lower bound: one decay per token multiplies whole rows, so no
  *    reciprocal is formed.  A token of -100 or below, -infinity among them,
  *    forgets all before it: its decay, and that over any tokens whose g sum to
- *    -100 or below, is exactly 0 (exp(-100) is 3.7e-44).  Values above 0 are outside the contract (fp32 uses them as
- *    given; bf16 results are unspecified).
+ *    -100 or below, is exactly 0 (exp(-100) is 3.7e-44).  Values above 0 are
+ *    outside the contract (fp32 uses them as given; bf16 results are unspecified).
  *  - Keys need not be unit vectors (their scale is taken out per row), but bf16
  *    prefill and backward want 0 <= beta |k|^2 <= 2, where no token's step enlarges
  *    the state (1/32 more is taken: unit keys and beta round to bf16), and

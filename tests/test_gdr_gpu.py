@@ -451,7 +451,7 @@ def test_the_debug_scan_reports_inputs_outside_the_contract(monkeypatch, dtype):
         for bad in (1e-3, float("nan"), math.inf):
             assert reports(3, bad, (0, 89, 3), back) and not reports(3, bad, (0, 90, 3), back)   # 90: of no sequence
         assert not reports(3, -math.inf, (0, 5, 0), back)
-        # a unit key times 1.42 is |k|^2 = 2.02, times 1.5 2.25; beta = 1
+        # a unit key times 1.4 is |k|^2 = 1.96, times 1.5 2.25; beta = 1
         one = lambda f: base[1][0, 40, 1] / base[1][0, 40, 1].float().norm().to(dtype) * f
         base[4][0, 40] = 1.0
         assert not reports(1, one(1.4), (0, 40, 1), back) and reports(1, one(1.5), (0, 40, 1), back) == (dtype == BF)
